@@ -326,6 +326,161 @@ nwc_status nwc_gemv_path(nwc_handle_t handle, const uint16_t* d_x, int32_t batch
 nwc_status nwc_gemv_noalloc(nwc_handle_t handle, const uint16_t* d_x, float* d_y,
                             int32_t batch, nwc_stream_t stream);
 
+/* ---- Around the projections: norms, rotation, paged cache, attention ------ */
+
+/* What a decode layer does between its q/k/v GEMV and its output GEMV.  These
+ * calls take no compressed matrix and no handle: every structure below is
+ * host memory that the call reads and does not keep (set struct_size =
+ * sizeof(the structure)); every pointer named d_... refers to memory of the
+ * current device.  They launch with programmatic stream serialization as the
+ * kernels above do, and read and write nothing before the previous kernel on the
+ * stream has completed.  They allocate nothing, so they can be captured into a
+ * graph; lengths and tables are read on the device at each replay. */
+
+/* Element types of nwc_heads and norm weights. */
+typedef enum { NWC_TYPE_BF16 = 0, NWC_TYPE_F32 = 1 } nwc_type;
+
+/* A tensor [tokens][heads][dim]: element (t, h, i) at data + (t token_stride +
+ * h head_stride + i) elements.  A part of a GEMV's y is one: token_stride is
+ * the rows of the matrix.  Strides in elements, any value >= 0 (outputs must
+ * not overlap themselves); data aligned to its element. */
+typedef struct {
+  uint32_t struct_size;
+  uint32_t type; /* nwc_type */
+  void* d_data;
+  int64_t token_stride, head_stride;
+} nwc_heads;
+
+/* Norm and rotation of heads of `dim` elements.  With weights w: x becomes
+ * x / sqrt(mean(x^2) + eps) w over a head (d_q_weight for q, d_k_weight for k,
+ * each may be NULL for no norm).  Then the first rotary_dim elements rotate by
+ * the angle t_i = position d_freq[i], i < rotary_dim / 2: pair i is elements
+ * (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved, and (a, b) becomes
+ * (a cos t - b sin t, b cos t + a sin t).  Sums and products in FP32, angles in
+ * 64 bits, one rounding to the output's type.  rotary_dim: a multiple of 8 up to
+ * dim, 0 for no rotation (d_freq is then not read). */
+typedef struct {
+  uint32_t struct_size;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  uint32_t weight_type; /* nwc_type of both weights */
+  const double* d_freq;
+  const void* d_q_weight;
+  const void* d_k_weight;
+  float eps; /* >= 0 */
+} nwc_rope;
+
+/* q_out[t] = rotate(norm(q[t]), positions[t]) and k_out likewise, t < tokens.
+ *   q, q_out: [tokens][heads][dim]; k, k_out: [tokens][kv_heads][dim].  q and k
+ *     have one type, q_out and k_out one type.  q (with q_out) or k (with k_out)
+ *     may be NULL.  In place (q_out = q with the same strides) is allowed.
+ *   d_positions: int32 [tokens], or int64 when positions_64 is non-zero; any
+ *     sign.
+ *   dim: a multiple of 8 up to 256.  tokens in [0, 2^24]; 0 launches nothing.
+ * Errors: INVALID_ARG, CUDA (launch). */
+nwc_status nwc_qk_norm_rope(const nwc_heads* q, const nwc_heads* k, const nwc_heads* q_out,
+                            const nwc_heads* k_out, int32_t tokens, int32_t heads,
+                            int32_t kv_heads, int32_t dim, const void* d_positions,
+                            int32_t positions_64, const nwc_rope* rope, nwc_stream_t stream);
+
+/* A paged cache: BF16 pages [pages][page_size][kv_heads][dim] for K and for V,
+ * element (p, s, h, i) at p page_stride + s token_stride + h head_stride + i.
+ * d_k, d_v 16-byte aligned, strides multiples of 8 elements.  page_size: a power
+ * of two from 8 to 2^20.  dim: a multiple of 8 up to 256.
+ * d_error: a device word, zero at first, that the kernels set bits of:
+ *   1 a bounded wait gave up, 4 a table or length named a page that is not there
+ *   (nwc_kv_get_error reads and clears it). */
+typedef struct {
+  uint32_t struct_size;
+  int32_t page_size, kv_heads, dim;
+  int64_t pages;
+  uint16_t* d_k;
+  uint16_t* d_v;
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+  uint32_t* d_error;
+} nwc_kv_cache;
+
+/* The sequences of a call, all tables int32 on the device.  Rows are
+ * sequences x new_tokens, the rows of one sequence together.
+ *   d_seq_lens[b]: tokens that sequence b has of its own, the call's new ones
+ *     among them; they live in pages d_block_table[b table_stride + n],
+ *     n < table_width, in order.
+ *   d_q_lens[b] (NULL: new_tokens for all): how many of its rows are real, from
+ *     the first; the others are padding.  Row i is own token
+ *     d_seq_lens[b] - d_q_lens[b] + i.
+ *   groups, d_group_start[groups + 1] (ascending): sequences
+ *     d_group_start[g] .. d_group_start[g + 1] - 1 share the prefix of
+ *     d_prefix_lens[g] tokens in pages d_prefix_table[g prefix_stride + n],
+ *     n < prefix_width, which comes before their own tokens.  Sequences in no
+ *     group have no prefix.  groups = 0: none has.
+ * Lengths below zero count as zero.  A token beyond its table, or on a page
+ * outside [0, pages), sets error bit 4: it is not appended, and attention sees
+ * no token past the table and zeros for the page.
+ * sequences x new_tokens <= 2^24; groups <= sequences. */
+typedef struct {
+  uint32_t struct_size;
+  int32_t sequences, new_tokens;
+  const int32_t* d_block_table;
+  int64_t table_stride;
+  int32_t table_width;
+  const int32_t* d_seq_lens;
+  const int32_t* d_q_lens;
+  int32_t groups;
+  const int32_t* d_group_start;
+  const int32_t* d_prefix_table;
+  int64_t prefix_stride;
+  int32_t prefix_width;
+  const int32_t* d_prefix_lens;
+} nwc_kv_batch;
+
+/* Appends the call's new tokens: K, normed and rotated, and V into the pages
+ * (rounded to BF16), and q, normed and rotated, into q_out, in one launch.  A
+ * token's position is its prefix's length plus its own index.
+ *   q, q_out: [rows][heads][dim], both or neither NULL; k, v:
+ *     [rows][kv_heads][dim]; q, k and v of one type.
+ * Padding rows of q_out are zero; nothing else of the cache is written.  Two
+ * rows must not name the same place.
+ * Errors: INVALID_ARG, CUDA (launch). */
+nwc_status nwc_kv_append(const nwc_kv_cache* cache, const nwc_kv_batch* batch,
+                         const nwc_heads* q, const nwc_heads* q_out, int32_t heads,
+                         const nwc_heads* k, const nwc_heads* v, const nwc_rope* rope,
+                         nwc_stream_t stream);
+
+/* Workspace of nwc_kv_attention for a batch of this shape (the lengths play no
+ * part): partial results of the parts that the key axis is split into.
+ * Errors: INVALID_ARG, UNSUPPORTED. */
+nwc_status nwc_kv_attention_workspace(const nwc_kv_cache* cache, const nwc_kv_batch* batch,
+                                      int32_t heads, uint64_t* bytes);
+
+/* out[r][h] = sum_j softmax_j(scale q[r][h] . K[j][g]) V[j][g], g = h kv_heads /
+ * heads, over the tokens j that row r sees: all of its prefix, then its own
+ * tokens up to and including itself.  A prefix is read once for all the rows
+ * that share it.
+ *   q, out: [rows][heads][dim], BF16, 16-byte aligned with strides of 8
+ *     elements.  heads: a multiple of kv_heads.  dim: 64 or 128 (others:
+ *     UNSUPPORTED).
+ *   d_lse (or NULL): FP32 [rows][heads], the natural logarithm of the sum of
+ *     exp(scale q . K) over the row's tokens.
+ *   d_workspace: at least nwc_kv_attention_workspace bytes, 256-byte aligned;
+ *     its contents need no initial value and are lost.  Calls whose work
+ *     overlaps must not share it.
+ * A row that sees no token, and a padding row, is zero with d_lse -infinity.
+ * Scores, sums and the running maximum are FP32; a probability is rounded to
+ * BF16 before it multiplies V.  Memory behind a sequence's or a prefix's last
+ * token is not used, whatever it holds.  The result is the same bit pattern on
+ * every run.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA (launch). */
+nwc_status nwc_kv_attention(const nwc_kv_cache* cache, const nwc_kv_batch* batch,
+                            const nwc_heads* q, int32_t heads, float scale,
+                            const nwc_heads* out, float* d_lse, void* d_workspace,
+                            uint64_t workspace_bytes, nwc_stream_t stream);
+
+/* Reads the cache's error word in order on `stream` (which it then synchronizes)
+ * and clears it.  Returns OK, DEVICE_TIMEOUT or INVALID_ARG (bit 4), in that
+ * order of precedence, or CUDA.  *word (optional) receives the raw bits. */
+nwc_status nwc_kv_get_error(const nwc_kv_cache* cache, nwc_stream_t stream, uint32_t* word);
+
 /* ---- Inspection, errors, teardown ------------------------------------- */
 
 /* Launch shape and schedule the kernels would use for a blob on a device with

@@ -4,11 +4,13 @@ The product is the C-ABI library libnwc.so (include/nwc.h); `_lib` binds it
 with ctypes (loaded on first use, and it raises if the library is missing).
 `synth` generates the seeded synthetic inputs; `autotune` picks a matrix's
 tile width and code limit by timing the library's GEMV on the device;
-`sharded` splits a matrix by output rows over a process group.
+`sharded` splits a matrix by output rows over a process group; `paged` holds
+what a decode layer does between its projections (norms with the position
+rotation, a paged key/value cache, attention over shared prefixes).
 """
 import importlib
 
-__all__ = ["CompressedMatrix", "lib"]
+__all__ = ["CompressedMatrix", "PagedBatch", "PagedKV", "lib"]
 
 
 def __getattr__(name):
@@ -16,4 +18,6 @@ def __getattr__(name):
         return importlib.import_module(__name__ + "._lib")
     if name == "CompressedMatrix":
         return importlib.import_module(__name__ + "._lib").CompressedMatrix
+    if name in ("PagedBatch", "PagedKV"):
+        return getattr(importlib.import_module(__name__ + ".paged"), name)
     raise AttributeError(name)

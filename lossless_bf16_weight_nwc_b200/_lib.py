@@ -57,6 +57,42 @@ class nwc_opts(ctypes.Structure):
                 ("streams", ctypes.c_uint32), ("keep", ctypes.c_uint32)]
 
 
+class nwc_heads(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("type", ctypes.c_uint32),
+                ("d_data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class nwc_rope(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("weight_type", ctypes.c_uint32),
+                ("d_freq", ctypes.c_void_p), ("d_q_weight", ctypes.c_void_p),
+                ("d_k_weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class nwc_kv_cache(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("pages", ctypes.c_int64), ("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("d_error", ctypes.c_void_p)]
+
+
+class nwc_kv_batch(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("sequences", ctypes.c_int32),
+                ("new_tokens", ctypes.c_int32), ("d_block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int32),
+                ("d_seq_lens", ctypes.c_void_p), ("d_q_lens", ctypes.c_void_p),
+                ("groups", ctypes.c_int32), ("d_group_start", ctypes.c_void_p),
+                ("d_prefix_table", ctypes.c_void_p), ("prefix_stride", ctypes.c_int64),
+                ("prefix_width", ctypes.c_int32), ("d_prefix_lens", ctypes.c_void_p)]
+
+
+NWC_TYPE_BF16, NWC_TYPE_F32 = 0, 1
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"libnwc.so not built ({LIB_PATH}); run "
@@ -90,6 +126,18 @@ def _load() -> ctypes.CDLL:
                                   c.c_int),
         "nwc_tc_schedule_describe": ([vp, u64, i32, u64, i32, c.POINTER(nwc_tc_schedule_info), vp,
                                       vp, vp, vp], c.c_int),
+        "nwc_qk_norm_rope": ([c.POINTER(nwc_heads)] * 4 + [i32] * 4 +
+                             [vp, i32, c.POINTER(nwc_rope), vp], c.c_int),
+        "nwc_kv_append": ([c.POINTER(nwc_kv_cache), c.POINTER(nwc_kv_batch),
+                           c.POINTER(nwc_heads), c.POINTER(nwc_heads), i32,
+                           c.POINTER(nwc_heads), c.POINTER(nwc_heads), c.POINTER(nwc_rope), vp],
+                          c.c_int),
+        "nwc_kv_attention_workspace": ([c.POINTER(nwc_kv_cache), c.POINTER(nwc_kv_batch), i32,
+                                        c.POINTER(u64)], c.c_int),
+        "nwc_kv_attention": ([c.POINTER(nwc_kv_cache), c.POINTER(nwc_kv_batch),
+                              c.POINTER(nwc_heads), i32, c.c_float, c.POINTER(nwc_heads), vp, vp,
+                              u64, vp], c.c_int),
+        "nwc_kv_get_error": ([c.POINTER(nwc_kv_cache), vp, c.POINTER(c.c_uint32)], c.c_int),
         "nwc_plan_destroy": ([vp], None),
         "nwc_handle_destroy": ([vp], None),
     }
@@ -108,6 +156,8 @@ EXPORTED = ("nwc_version", "nwc_status_string", "nwc_plan", "nwc_plan_size", "nw
             "nwc_gemv_noalloc", "nwc_gemv_set_tc_min_batch", "nwc_gemv_path",
             "nwc_handle_info", "nwc_get_device_error", "nwc_test_set_wait_limit",
             "nwc_schedule_describe", "nwc_tc_schedule_describe",
+            "nwc_qk_norm_rope", "nwc_kv_append", "nwc_kv_attention_workspace",
+            "nwc_kv_attention", "nwc_kv_get_error",
             "nwc_plan_destroy", "nwc_handle_destroy")
 
 
@@ -297,6 +347,43 @@ def nwc_tc_schedule_describe(blob: np.ndarray, sm_count: int = 148, smem_limit: 
            "nwc_tc_schedule_describe")
     d = {k: getattr(info, k) for k, _ in nwc_tc_schedule_info._fields_ if k != "struct_size"}
     return d, cta, bat, ring, tb
+
+
+# The structures of the calls below are passed by reference and read before the
+# call returns; q, q_out and k of nwc_qk_norm_rope and nwc_kv_append may be None.
+
+def nwc_qk_norm_rope(q, k, q_out, k_out, tokens: int, heads: int, kv_heads: int, dim: int,
+                     d_positions, positions_64: bool, rope, stream=None) -> None:
+    _check(LIB.nwc_qk_norm_rope(q, k, q_out, k_out, tokens, heads, kv_heads, dim,
+                                _ptr(d_positions), positions_64, rope, _stream(stream)),
+           "nwc_qk_norm_rope")
+
+
+def nwc_kv_append(cache, batch, q, q_out, heads: int, k, v, rope, stream=None) -> None:
+    _check(LIB.nwc_kv_append(cache, batch, q, q_out, heads, k, v, rope, _stream(stream)),
+           "nwc_kv_append")
+
+
+def nwc_kv_attention_workspace(cache, batch, heads: int) -> int:
+    out = ctypes.c_uint64()
+    _check(LIB.nwc_kv_attention_workspace(cache, batch, heads, ctypes.byref(out)),
+           "nwc_kv_attention_workspace")
+    return out.value
+
+
+def nwc_kv_attention(cache, batch, q, heads: int, scale: float, out, d_lse, d_workspace,
+                     workspace_bytes: int, stream=None) -> None:
+    _check(LIB.nwc_kv_attention(cache, batch, q, heads, scale, out,
+                                None if d_lse is None else _ptr(d_lse), _ptr(d_workspace),
+                                workspace_bytes, _stream(stream)), "nwc_kv_attention")
+
+
+def nwc_kv_get_error(cache, stream=None) -> tuple[int, int]:
+    """(status, raw word) of a cache's device error word, read and cleared in
+    order on the stream, which it synchronizes."""
+    w = ctypes.c_uint32()
+    st = LIB.nwc_kv_get_error(cache, _stream(stream), ctypes.byref(w))
+    return st, w.value
 
 
 def nwc_plan_destroy(plan) -> None:

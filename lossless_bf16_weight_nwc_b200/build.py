@@ -13,7 +13,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libnwc.so")
-SOURCES = ["kernels.cu", "nwc_api.cu", "encoder.cpp", "schedule.cpp"]
+SOURCES = ["kernels.cu", "nwc_api.cu", "rope.cu", "attention.cu", "paged_api.cu", "encoder.cpp",
+           "schedule.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -41,7 +42,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-Xcompiler", "-pthread", "-cudart", "static", "-I", os.path.join(ROOT, "include"),
+           "-Xcompiler", "-pthread", "--threads", "0", "-cudart", "static", "-I", os.path.join(ROOT, "include"),
            "-o", tmp, *[os.path.join(CSRC, s) for s in SOURCES]]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

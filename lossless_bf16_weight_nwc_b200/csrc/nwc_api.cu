@@ -17,6 +17,7 @@
 
 #include "../../include/nwc.h"
 #include "kernels.cuh"
+#include "nwc_device.h"
 #include "nwc_internal.h"
 
 namespace {
@@ -33,7 +34,10 @@ std::atomic<uint32_t> g_wait_limit{0};
 
 nwc_status cuda_status(cudaError_t e) { return e == cudaSuccess ? NWC_OK : NWC_ERR_CUDA; }
 
-// SM count and per-block opt-in shared memory of the current device (cached).
+}  // namespace
+
+namespace nwc {
+
 nwc_status current_device(int* dev, int* sms, size_t* smem) {
   cudaError_t e = cudaGetDevice(dev);
   if (e != cudaSuccess) return NWC_ERR_CUDA;
@@ -52,6 +56,29 @@ nwc_status current_device(int* dev, int* sms, size_t* smem) {
   *smem = (size_t)g_smem_optin[*dev];
   return NWC_OK;
 }
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+uint32_t wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
+}  // namespace nwc
+
+namespace {
+
+using nwc::current_device;
+using nwc::tensor_map_encoder;
 
 // The code kind the kernels read for a handle, and the table bytes a CTA loads.
 int code_of(const nwc_handle_s& h) {
@@ -608,21 +635,6 @@ nwc_status gemv_check(const nwc_handle_s* h, const uint16_t* d_x, const float* d
   if (cudaGetDevice(&dev) != cudaSuccess) return NWC_ERR_CUDA;
   if (dev != h->device) return NWC_ERR_INVALID_ARG;
   return NWC_OK;
-}
-
-// cuTensorMapEncodeTiled from the driver, looked up once.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
 }
 
 // Whether a GEMV of `batch` rows takes the tensor-core kernel: at or above the

@@ -1,0 +1,84 @@
+// paged.cuh — parameters and launch interface of the kernels around the paged
+// key/value cache (host side).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "kernels.cuh"
+
+namespace nwc {
+
+// A tensor [tokens, heads, dim] read or written by the kernels: the last
+// dimension contiguous, the others at any stride (in elements).
+struct HeadsView {
+  void* data;
+  int64_t token_stride, head_stride;
+};
+
+// The cache: K and V pages of page_size tokens x kv_heads x dim BF16.
+struct CacheView {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t k_page, k_token, k_head;  // strides in elements
+  int64_t v_page, v_token, v_head;
+  int64_t pages;
+  int32_t page_shift;               // log2(page_size)
+  uint32_t* err;                    // device: the cache's error word
+};
+
+// The batch's tables (all int32 on the device).
+struct BatchView {
+  int32_t sequences, chunk;         // rows of the batch: sequences x chunk
+  const int32_t* table;             // own pages, [sequences] rows of table_width
+  int64_t table_stride;
+  int32_t table_width;
+  const int32_t* lens;              // own tokens, the new ones among them
+  const int32_t* q_lens;            // new tokens of each sequence; null: chunk
+  int32_t groups;                   // shared prefixes; 0: none
+  const int32_t* group_start;       // [groups + 1]
+  const int32_t* prefix_table;
+  int64_t prefix_stride;
+  int32_t prefix_width;
+  const int32_t* prefix_lens;       // [groups]
+};
+
+enum : int32_t { kTypeBf16 = 0, kTypeF32 = 1 };
+
+// Norms and rotation of heads, and where they go: to output tensors
+// (append == false, positions given) or q to its tensor and k, v to the cache.
+struct RopeParams {
+  HeadsView q, k, v;          // inputs; q.data or k.data may be null
+  HeadsView q_out, k_out;     // outputs of the same shapes
+  int32_t tokens, heads, kv_heads, dim;
+  int32_t rotary;             // leading elements of a head that rotate; 0: none
+  int32_t interleaved;        // pairs (2i, 2i + 1), else (i, i + rotary / 2)
+  const double* freq;         // [rotary / 2] radians a position
+  const void* q_weight;       // [dim] or null: no norm
+  const void* k_weight;
+  int32_t weight_f32;
+  float eps;
+  const void* positions;      // [tokens] int32 or int64 (append == false)
+  int32_t positions_64;
+  int32_t append;
+  CacheView cache;
+  BatchView batch;
+};
+cudaError_t launch_rope(const RopeParams& p, int in_type, int out_type, int sm_count,
+                        cudaStream_t stream);
+
+struct AttentionParams {
+  HeadsView q, out;           // BF16 [rows][heads][dim]
+  int32_t heads, kv_heads, dim;
+  float scale;
+  float* lse;                 // [rows][heads] or null
+  CacheView cache;
+  BatchView batch;
+  void* workspace;
+  uint32_t wait_limit;        // polls before a bounded wait gives up (0: default)
+};
+uint64_t attention_workspace(int sequences, int chunk, int groups, int heads, int kv_heads,
+                             int dim, int sm_count);
+cudaError_t launch_attention(const AttentionParams& p, int sm_count, cudaStream_t stream);
+
+}  // namespace nwc

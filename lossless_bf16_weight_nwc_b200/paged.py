@@ -1,0 +1,425 @@
+"""What a decode layer does between its compressed projections: per-head norms
+with the position rotation, a paged key/value cache, and attention over it for
+a batch whose sequences may share prefixes.
+
+A layer's step with a fused q/k/v matrix (`CompressedMatrix.compress_fused`):
+
+    y = wqkv.gemv(x)                                   # FP32 [rows, ...]
+    q, k, v = (t.unflatten(-1, (-1, dim)) for t in wqkv.split(y))
+    q = cache.append(batch, k, v, q=q, freq=freq, q_weight=qn, k_weight=kn)
+    o = cache.attend(batch, q)                         # BF16 [rows, heads, dim]
+    y = wo.gemv(o.flatten(1))
+
+`AttentionBlock` holds those pieces for one layer.  All of it runs in libnwc's
+kernels; lengths and tables stay on the device, so a step can be captured into a
+CUDA graph and replayed as they change.  Nothing here has a gradient: inputs
+that require one are refused while gradients are recorded.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import _lib
+
+_TYPES = {torch.bfloat16: _lib.NWC_TYPE_BF16, torch.float32: _lib.NWC_TYPE_F32}
+_HEADS = ctypes.sizeof(_lib.nwc_heads)
+
+
+def rope_frequencies(rotary_dim: int, theta: float = 10000.0, device="cuda",
+                     factor: float = 1.0, low_freq_factor: float = 1.0,
+                     high_freq_factor: float = 4.0, original_positions: int = 8192):
+    """FP64 [rotary_dim / 2] radians a position, theta^(-2i / rotary_dim).  factor
+    > 1 stretches them as Llama-3.1's configuration does: frequencies of fewer
+    than low_freq_factor turns over original_positions are divided by factor,
+    those of more than high_freq_factor kept, those between interpolated."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim: an even number")
+    f = theta ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    if factor != 1.0:
+        turns = original_positions * f / (2 * math.pi)
+        keep = ((turns - low_freq_factor) / (high_freq_factor - low_freq_factor)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    return f.to(device)
+
+
+def _no_grad(*tensors) -> None:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError("an input requires a gradient, which these kernels do not give; "
+                         "call under torch.no_grad()")
+
+
+def _heads(t, what: str, shape, device, dtypes=_TYPES):
+    """The C view of a tensor [tokens, heads, dim] with any strides but a
+    contiguous last dimension."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    return _lib.nwc_heads(_HEADS, _TYPES[t.dtype], t.data_ptr(), st[0] if shape[0] > 1 else 0,
+                          st[1] if shape[1] > 1 else 0)
+
+
+def _output(t, what: str, shape, device, dtypes):
+    h = _heads(t, what, shape, device, dtypes)
+    rows, heads, dim = shape
+    ts, hs = h.token_stride, h.head_stride
+    if not ((heads == 1 or hs >= dim) and (rows == 1 or ts >= dim) and
+            (heads == 1 or rows == 1 or ts >= heads * hs or hs >= rows * ts)) and rows:
+        raise ValueError(f"{what}: its elements overlap")
+    return h
+
+
+def _vector(t, what: str, device, n: int, dtypes) -> int:
+    """The address of a contiguous vector of n elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous elements, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _rope(dim: int, device, freq, q_weight, k_weight, eps: float, interleaved: bool):
+    r = _lib.nwc_rope(ctypes.sizeof(_lib.nwc_rope), 0, interleaved, 0, None, None, None, eps)
+    if not 0 <= eps < math.inf:
+        raise ValueError("eps: a finite number, not negative")
+    if freq is not None:
+        n = freq.numel() if isinstance(freq, torch.Tensor) else 0
+        r.d_freq = _vector(freq, "freq", device, n, (torch.float64,))
+        if 2 * n > dim or n % 4:
+            raise ValueError(f"freq: {n} elements; a multiple of 4 up to {dim // 2}")
+        r.rotary_dim = 2 * n
+    types = {w.dtype for w in (q_weight, k_weight) if isinstance(w, torch.Tensor)}
+    if len(types) > 1:
+        raise TypeError("q_weight and k_weight: expected one dtype")
+    if q_weight is not None:
+        r.d_q_weight = _vector(q_weight, "q_weight", device, dim, _TYPES)
+    if k_weight is not None:
+        r.d_k_weight = _vector(k_weight, "k_weight", device, dim, _TYPES)
+    if types:
+        r.weight_type = _TYPES[types.pop()]
+    return r
+
+
+def _on(device, stream, call):
+    """call() with the device current and, when a stream is given, that stream
+    current too: what the call allocates then belongs to the stream it runs on."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return call()
+        with torch.cuda.device(device):
+            return call()
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(getattr(stream, "cuda_stream", stream))
+        stream = (torch.cuda.ExternalStream(raw, device=device) if raw
+                  else torch.cuda.default_stream(device))
+    if stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, expected {device}")
+    with torch.cuda.stream(stream):
+        return call()
+
+
+def _cuda(t, what: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{what}: on {t.device}, expected a CUDA device")
+    return t.device
+
+
+def qk_norm_rope(q, k, positions, freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, out=None, stream=None):
+    """(q_out, k_out): each head of q [tokens, heads, dim] and k [tokens,
+    kv_heads, dim] divided by its root mean square and times its weight (where
+    one is given), then rotated by positions [tokens] x freq (FP64, from
+    rope_frequencies; None: no rotation) in pairs (i, i + rotary / 2), or
+    (2i, 2i + 1) when interleaved.  q and k are FP32 or BF16 with any strides but
+    a contiguous last dimension (views of a GEMV's result); either may be None.
+    The results are BF16, or what `out` (a pair of tensors, also q and k
+    themselves) holds."""
+    first = q if q is not None else k
+    device = _cuda(first, "q" if q is not None else "k")
+    _no_grad(q, k, q_weight, k_weight, freq)
+    if first.dim() != 3:
+        raise ValueError("q, k: expected [tokens, heads, dim]")
+    tokens, _, dim = first.shape
+    pair = []
+    for t, what in ((q, "q"), (k, "k")):
+        if t is None:
+            pair.append((0, None))
+            continue
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{what}: expected a tensor [tokens, heads, dim]")
+        pair.append((t.shape[1], _heads(t, what, (tokens, t.shape[1], dim), device)))
+    if q is not None and k is not None and q.dtype != k.dtype:
+        raise TypeError("q and k: expected one dtype")
+    if not 8 <= dim <= 256 or dim % 8:
+        raise ValueError(f"dim {dim}: a multiple of 8 from 8 to 256")
+    rope = _rope(dim, device, freq, q_weight, k_weight, eps, interleaved)
+    at = _vector(positions, "positions", device, tokens, (torch.int32, torch.int64))
+    if out is not None and (len(out) != 2 or any((o is None) != (t is None)
+                                                 for o, t in zip(out, (q, k)))):
+        raise ValueError("out: a pair of tensors for q and k, None where the input is None")
+
+    def call():
+        res = out if out is not None else [
+            None if t is None else torch.empty(t.shape, dtype=torch.bfloat16, device=device)
+            for t in (q, k)]
+        to = [None if o is None else _output(o, f"{w}_out", t.shape, device, _TYPES)
+              for o, t, w in zip(res, (q, k), "qk")]
+        if to[0] is not None and to[1] is not None and to[0].type != to[1].type:
+            raise TypeError("out: expected one dtype")
+        if tokens:
+            _lib.nwc_qk_norm_rope(pair[0][1], pair[1][1], to[0], to[1], tokens, pair[0][0],
+                                  pair[1][0], dim, at, positions.dtype == torch.int64, rope)
+        return tuple(res)
+
+    return _on(device, stream, call)
+
+
+class PagedBatch:
+    """The sequences of a call and where their tokens are.
+
+    block_table  int32 [sequences, width]: sequence b's own pages, in order.
+    seq_lens     int32 [sequences]: own tokens, a call's new ones among them.
+    q_lens       int32 [sequences] or None: how many of a sequence's rows are
+                 new tokens, from its first row; the others are padding.
+    prefix_table int32 [groups, width], prefix_lens int32 [groups], group_start
+                 int32 [groups + 1]: sequences group_start[g] up to
+                 group_start[g + 1] share prefix g, which comes before their own
+                 tokens; all three or none.
+
+    All on one CUDA device; their contents are read when a kernel runs, so they
+    may be changed in place between calls.  Entries behind a sequence's last page
+    are not read."""
+
+    def __init__(self, block_table, seq_lens, q_lens=None, prefix_table=None, prefix_lens=None,
+                 group_start=None):
+        self.device = _cuda(block_table, "block_table")
+        self._keep = (block_table, seq_lens, q_lens, prefix_table, prefix_lens, group_start)
+        i32 = (torch.int32,)
+        table = self._table(block_table, "block_table")
+        self.sequences = block_table.shape[0]
+        lens = _vector(seq_lens, "seq_lens", self.device, self.sequences, i32)
+        fresh = None if q_lens is None else _vector(q_lens, "q_lens", self.device,
+                                                    self.sequences, i32)
+        if len({x is None for x in (prefix_table, prefix_lens, group_start)}) != 1:
+            raise ValueError("prefix_table, prefix_lens, group_start: all three or none")
+        self.groups = 0
+        far = (0, None, None, 0, 0, None)
+        if prefix_table is not None and prefix_table.shape[0]:
+            shared = self._table(prefix_table, "prefix_table")
+            self.groups = prefix_table.shape[0]
+            if self.groups > self.sequences:
+                raise ValueError(f"{self.groups} groups of {self.sequences} sequences")
+            far = (self.groups,
+                   _vector(group_start, "group_start", self.device, self.groups + 1, i32),
+                   *shared,
+                   _vector(prefix_lens, "prefix_lens", self.device, self.groups, i32))
+        self._fields = (*table, lens, fresh, *far)
+        self._views = {}
+
+    def _table(self, t, what: str):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 2:
+            raise TypeError(f"{what}: expected an int32 tensor [rows, width]")
+        if t.device != self.device:
+            raise ValueError(f"{what}: on {t.device}, expected {self.device}")
+        if t.shape[0] and (t.shape[1] < 1 or (t.stride(1) != 1 and t.shape[1] > 1)):
+            raise ValueError(f"{what}: its rows must be contiguous and not empty")
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.shape[1]
+
+    def _view(self, rows: int):
+        """The C view for calls of `rows` rows in all."""
+        view = self._views.get(rows)
+        if view is None:
+            chunk = rows // self.sequences if self.sequences else 1
+            if chunk < 1 or (chunk * self.sequences != rows):
+                raise ValueError(f"{rows} rows for {self.sequences} sequences: the same number, "
+                                 "at least one, for each")
+            if rows > 1 << 24:
+                raise ValueError(f"{rows} rows; a call takes up to 2^24")
+            view = _lib.nwc_kv_batch(ctypes.sizeof(_lib.nwc_kv_batch), self.sequences, chunk,
+                                     *self._fields)
+            self._views[rows] = view
+        return view
+
+
+class PagedKV:
+    """A paged key/value cache over the caller's pages: k_pages and v_pages BF16
+    [pages, page_size, kv_heads, dim] on one CUDA device, the last dimension
+    contiguous, other strides multiples of 8 elements, 16-byte aligned (a
+    permuted view gives pages that keep each head's tokens together).
+    page_size: a power of two, 8 or more.
+
+    Calls run on the device's current torch stream, or the stream given; append
+    and attend on the same pages must be ordered by the caller."""
+
+    def __init__(self, k_pages, v_pages):
+        self.device = _cuda(k_pages, "k_pages")
+        for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 4:
+                raise TypeError(f"{what}: expected a BF16 tensor [pages, page_size, kv_heads, dim]")
+            if t.device != self.device or t.shape != k_pages.shape:
+                raise ValueError(f"{what}: {tuple(t.shape)} on {t.device}, expected "
+                                 f"{tuple(k_pages.shape)} on {self.device}")
+        _no_grad(k_pages, v_pages)
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.pages, self.page_size, self.kv_heads, self.dim = k_pages.shape
+        if self.page_size < 8 or self.page_size & (self.page_size - 1):
+            raise ValueError(f"page_size {self.page_size}: a power of two, 8 or more")
+        if not 8 <= self.dim <= 256 or self.dim % 8:
+            raise ValueError(f"dim {self.dim}: a multiple of 8 from 8 to 256")
+        if self.pages < 1 or self.kv_heads < 1:
+            raise ValueError("k_pages: no pages")
+        strides = []
+        for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            st = [s if n > 1 else 8 for s, n in zip(t.stride(), t.shape)]
+            if t.stride(3) != 1 or any(s % 8 or s < 8 for s in st[:3]) or t.data_ptr() % 16:
+                raise ValueError(f"{what}: needs a contiguous last dimension, other strides of "
+                                 "multiples of 8 elements, and 16-byte alignment")
+            strides += st[:3]
+        with torch.cuda.device(self.device):
+            self._error = torch.zeros(1, dtype=torch.int32, device=self.device)
+            torch.cuda.current_stream().synchronize()  # zero before any stream's kernel
+        self._view = _lib.nwc_kv_cache(ctypes.sizeof(_lib.nwc_kv_cache), self.page_size,
+                                       self.kv_heads, self.dim, self.pages, k_pages.data_ptr(),
+                                       v_pages.data_ptr(), *strides, self._error.data_ptr())
+        self._workspace = {}
+
+    def device_error(self, stream=None) -> tuple[int, int]:
+        """(status, raw word) of this cache's device error word (read and cleared):
+        bit 1 a bounded wait gave up, bit 4 a table or length named a page that is
+        not there."""
+        with torch.cuda.device(self.device):
+            return _lib.nwc_kv_get_error(self._view, stream)
+
+    def _rows(self, batch, t, what: str):
+        if not isinstance(batch, PagedBatch):
+            raise TypeError(f"batch: expected a PagedBatch, got {type(batch).__name__}")
+        if batch.device != self.device:
+            raise ValueError(f"batch: on {batch.device}, expected {self.device}")
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{what}: expected a tensor [rows, heads, dim]")
+        return t.shape[0], batch._view(t.shape[0])
+
+    def append(self, batch: PagedBatch, k, v, q=None, freq=None, q_weight=None, k_weight=None,
+               eps: float = 1e-6, interleaved: bool = False, q_out=None, stream=None):
+        """Appends the new tokens' k (normed and rotated as in qk_norm_rope, at the
+        position of its token: the prefix's length plus its own index) and v, both
+        [rows, kv_heads, dim], to their sequences' pages, and returns q [rows,
+        heads, dim], normed and rotated likewise, as BF16 (None without q).  Inputs
+        FP32 or BF16, one type, with any strides but a contiguous last dimension.
+        seq_lens counts the new tokens already.  Padding rows are not appended,
+        their q is zero."""
+        rows, view = self._rows(batch, k, "k")
+        _no_grad(q, k, v, q_weight, k_weight, freq)
+        device = self.device
+        kh = _heads(k, "k", (rows, self.kv_heads, self.dim), device)
+        vh = _heads(v, "v", (rows, self.kv_heads, self.dim), device, (k.dtype,))
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out: given without q")
+            heads, qh = 1, None
+        else:
+            if not isinstance(q, torch.Tensor) or q.dim() != 3:
+                raise ValueError("q: expected a tensor [rows, heads, dim]")
+            heads = q.shape[1]
+            qh = _heads(q, "q", (rows, heads, self.dim), device, (k.dtype,))
+        rope = _rope(self.dim, device, freq, q_weight, k_weight, eps, interleaved)
+
+        def call():
+            out = q_out
+            if q is not None and out is None:
+                out = torch.empty((rows, heads, self.dim), dtype=torch.bfloat16, device=device)
+            oh = None if out is None else _output(out, "q_out", (rows, heads, self.dim), device,
+                                                  (torch.bfloat16,))
+            if rows:
+                _lib.nwc_kv_append(self._view, view, qh, oh, heads, kh, vh, rope)
+            return out
+
+        return _on(device, stream, call)
+
+    def attend(self, batch: PagedBatch, q, scale: float | None = None, out=None,
+               return_lse: bool = False, stream=None):
+        """softmax(scale q K^T) V for q BF16 [rows, heads, dim] (heads a multiple of
+        kv_heads; dim 64 or 128; scale None: 1 / sqrt(dim)): each row sees its
+        prefix and its sequence's own tokens up to itself.  BF16 of q's shape;
+        with return_lse also FP32 [rows, heads], the logarithm of the sum of
+        exponentials.  A row that sees nothing, and a padding row, is zero (-inf)."""
+        rows, view = self._rows(batch, q, "q")
+        _no_grad(q)
+        if self.dim not in (64, 128):
+            raise ValueError(f"dim {self.dim}: attention takes heads of 64 or 128")
+        heads = q.shape[1]
+        if heads < 1 or heads % self.kv_heads:
+            raise ValueError(f"q: {heads} heads, expected a multiple of {self.kv_heads}")
+        bf16 = (torch.bfloat16,)
+        qh = _heads(q, "q", (rows, heads, self.dim), self.device, bf16)
+        if qh.d_data and (qh.d_data % 16 or qh.token_stride % 8 or qh.head_stride % 8):
+            raise ValueError("q: needs 16-byte alignment and strides of multiples of 8 elements")
+        if scale is None:
+            scale = 1.0 / math.sqrt(self.dim)
+
+        def call():
+            o = torch.empty((rows, heads, self.dim), dtype=torch.bfloat16,
+                            device=self.device) if out is None else out
+            oh = _output(o, "out", (rows, heads, self.dim), self.device, bf16)
+            lse = torch.empty((rows, heads), dtype=torch.float32,
+                              device=self.device) if return_lse else None
+            if rows:
+                key = (rows, batch.sequences, batch.groups, heads)
+                need = self._workspace.get(key)
+                if need is None:
+                    need = _lib.nwc_kv_attention_workspace(self._view, view, heads)
+                    self._workspace[key] = need
+                # From torch's allocator on the call's stream: calls on different
+                # streams, and captured graphs, each have their own.
+                ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+                _lib.nwc_kv_attention(self._view, view, qh, heads, scale, oh, lse, ws, need)
+            return (o, lse) if return_lse else o
+
+        return _on(self.device, stream, call)
+
+
+class AttentionBlock:
+    """One layer's attention over compressed projections: wqkv, a fused matrix of
+    the q, k and v rows (`CompressedMatrix.compress_fused([wq, wk, wv])`), and wo.
+
+    step(x, batch) appends x's tokens to the layer's cache and returns the output
+    projection FP32 [rows, wo.rows]; q_weight and k_weight are the per-head norms
+    of models that have them."""
+
+    def __init__(self, wqkv, wo, cache: PagedKV, freq, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, interleaved: bool = False, scale: float | None = None):
+        b = wqkv.row_splits
+        width = cache.kv_heads * cache.dim
+        if len(b) != 4 or b[2] - b[1] != width or b[3] - b[2] != width or b[1] % cache.dim:
+            raise ValueError(f"wqkv: row splits {b} do not fit {cache.kv_heads} key heads of "
+                             f"{cache.dim}")
+        if wo.cols != b[1]:
+            raise ValueError(f"wo: {wo.cols} columns, expected {b[1]}")
+        self.wqkv, self.wo, self.cache, self.freq = wqkv, wo, cache, freq
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
+        self.interleaved, self.scale = interleaved, scale
+
+    def step(self, x, batch: PagedBatch):
+        """x BF16 [rows, wqkv.cols], 1 to 64 rows, a sequence's rows together."""
+        dim = self.cache.dim
+        q, k, v = (t.unflatten(-1, (-1, dim)) for t in self.wqkv.split(self.wqkv.gemv(x)))
+        q = self.cache.append(batch, k, v, q=q, freq=self.freq, q_weight=self.q_weight,
+                              k_weight=self.k_weight, eps=self.eps,
+                              interleaved=self.interleaved)
+        return self.wo.gemv(self.cache.attend(batch, q, scale=self.scale).flatten(1))

@@ -1,0 +1,513 @@
+"""The operators between a layer's projections on the GPU, against plain 64-bit
+forms (paged_reference.py derives the bounds): norms with the rotation, the
+paged append, and attention over shared prefixes, alone and as a layer runs
+them together."""
+import math
+
+import numpy as np
+import pytest
+
+import paged_reference as ref
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def paged():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from lossless_bf16_weight_nwc_b200 import build
+    build.build()
+    from lossless_bf16_weight_nwc_b200 import paged as module
+    torch.cuda.set_device(0)
+    return module
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+# ---- norms and rotation -----------------------------------------------------
+
+QK = [  # tokens, heads, kv_heads, dim, rotary, interleaved, weights, in, out
+    (1, 32, 8, 128, 128, False, "bf16", "f32", "bf16"),
+    (1, 1, 1, 8, 8, False, None, "bf16", "bf16"),
+    (3, 5, 1, 64, 64, True, "f32", "bf16", "bf16"),
+    (2, 3, 2, 80, 40, False, "bf16", "f32", "f32"),
+    (65, 28, 4, 96, 96, True, "bf16", "f32", "bf16"),
+    (7, 2, 2, 256, 256, False, "f32", "bf16", "f32"),
+    (33, 9, 3, 256, 64, True, None, "f32", "bf16"),
+    (5, 4, 4, 104, 48, False, "bf16", "bf16", "bf16"),
+    (17, 8, 2, 128, 0, False, "bf16", "f32", "bf16"),
+    (701, 32, 8, 128, 128, False, "bf16", "bf16", "bf16"),
+    (2050, 10, 2, 64, 32, True, "f32", "f32", "bf16"),
+    (1500, 24, 8, 256, 256, False, None, "f32", "f32"),
+]
+DT = {"bf16": torch.bfloat16, "f32": torch.float32} if torch else {}
+
+
+def weights(g, kind, dim):
+    return None if kind is None else (1 + 0.3 * randn(g, dim)).to(DT[kind])
+
+
+@pytest.mark.parametrize("tokens,h,hk,dim,rotary,inter,wkind,tin,tout", QK)
+def test_qk_norm_rope(paged, tokens, h, hk, dim, rotary, inter, wkind, tin, tout):
+    g = gen(tokens + dim)
+    y = (3 * randn(g, tokens, (h + 2 * hk) * dim)).to(DT[tin])
+    q, k = y[:, :h * dim].unflatten(1, (h, dim)), y[:, h * dim:-hk * dim].unflatten(1, (hk, dim))
+    pos = torch.randint(0, 200000, (tokens,), generator=g, device="cuda",
+                        dtype=torch.int64 if tokens % 2 else torch.int32)
+    freq = paged.rope_frequencies(rotary, 1e4) if rotary else None
+    qw, kw = weights(g, wkind, dim), weights(g, wkind, dim)
+    out = [torch.full(t.shape, math.nan, dtype=DT[tout], device="cuda") for t in (q, k)]
+    before = y.clone()
+    a, b = paged.qk_norm_rope(q, k, pos, freq, qw, kw, eps=1e-5, interleaved=inter, out=out)
+    assert a is out[0] and b is out[1]
+    for got, x, w in ((a, q, qw), (b, k, kw)):
+        want, bound = ref.norm_rotate(x, w, pos, freq, inter, 1e-5)
+        assert ref.close(got, want, bound, DT[tout])
+    assert torch.equal(y, before)
+
+
+def test_qk_far_and_negative_positions(paged):
+    g = gen(1)
+    pos = torch.tensor([0, -1, -5000, 2 ** 31 - 1, 2 ** 40 + 3, 10 ** 6], device="cuda")
+    q = randn(g, 6, 4, 128)
+    freq = paged.rope_frequencies(128, 5e5)
+    a, none = paged.qk_norm_rope(q, None, pos, freq)
+    assert none is None and a.dtype == torch.bfloat16
+    want, bound = ref.norm_rotate(q, None, pos, freq, False, 0)
+    # The definition's own angle is known to 2^-53 of 2^40 turns.
+    assert ref.close(a, want, bound + 2.0 ** -12 * q.abs().amax(), torch.bfloat16)
+    assert ref.close(a[[0, 1, 2, 5]], want[[0, 1, 2, 5]], bound[[0, 1, 2, 5]], torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_qk_strides_alignment_and_in_place(paged, dtype):
+    g = gen(2)
+    freq = paged.rope_frequencies(64, 1e4)
+    pos = torch.arange(9, device="cuda")
+    # Odd row length, odd start, heads before tokens, a broadcast token.
+    base = randn(g, 9, 4 * 64 + 1).to(DT[dtype])
+    odd = base[:, 1:].unflatten(1, (4, 64))
+    flat = randn(g, 4 * 9 * 64 + 3).to(DT[dtype])[3:].view(4, 9, 64).transpose(0, 1)
+    wide = randn(g, 1, 4, 64).to(DT[dtype]).expand(9, 4, 64)
+    for q in (odd, flat, wide):
+        want, bound = ref.norm_rotate(q, None, pos, freq, False, 0)
+        got, _ = paged.qk_norm_rope(q, None, pos, freq)
+        assert ref.close(got, want, bound, torch.bfloat16)
+        store = torch.zeros(9 * 4 * 65 + 1, dtype=DT[dtype], device="cuda")
+        out = store[1:].view(9, 4, 65)[..., :64]
+        paged.qk_norm_rope(q, None, pos, freq, out=(out, None))
+        assert ref.close(out, want, bound, DT[dtype])
+        assert not store[1:].view(9, 4, 65)[..., 64].any()
+    want, bound = ref.norm_rotate(odd, None, pos, freq, False, 0)
+    paged.qk_norm_rope(odd, None, pos, freq, out=(odd, None))      # in place
+    assert ref.close(odd, want, bound, DT[dtype])
+
+
+def test_qk_empty_and_special_values(paged):
+    freq = paged.rope_frequencies(64, 1e4)
+    q = torch.zeros((0, 4, 64), dtype=torch.float32, device="cuda")
+    a, b = paged.qk_norm_rope(q, q, torch.zeros(0, dtype=torch.int32, device="cuda"), freq)
+    assert a.shape == (0, 4, 64) and b.dtype == torch.bfloat16
+    g = gen(3)
+    x = randn(g, 3, 2, 64)
+    x[0, 0, 5], x[1, 1, 7], x[2, 0] = math.nan, math.inf, 0.0
+    w = torch.ones(64, device="cuda")
+    a, _ = paged.qk_norm_rope(x, None, ints([4, 5, 6]), freq, w)
+    good = torch.ones(3, 2, dtype=torch.bool)
+    good[0, 0] = good[1, 1] = False
+    want, bound = ref.norm_rotate(x, w, ints([4, 5, 6]), freq, False, 1e-6)
+    assert torch.isnan(a[0, 0]).all() and not a[2, 0].any()
+    assert torch.isnan(a[1, 1, 7]) and ref.close(a[good], want[good], bound[good], torch.bfloat16)
+
+
+# ---- cache helpers ----------------------------------------------------------
+
+class Case:
+    """A cache with stale NaN behind every sequence's and prefix's last token."""
+
+    def __init__(self, paged, seed, lens, kv_heads=2, dim=64, page=16, prefix=None, starts=None,
+                 q_lens=None, heads_first=False, extra=2, poison=True, width=None):
+        self.g = g = gen(seed)
+        self.lens, self.q_lens, self.prefix, self.starts = lens, q_lens, prefix, starts
+        count = [-(-max(n, 0) // page) for n in lens + (prefix or [])]
+        pool = sum(count) + extra
+        shape = (pool, kv_heads, page, dim) if heads_first else (pool, page, kv_heads, dim)
+        k, v = randn(g, *shape).bfloat16(), randn(g, *shape).bfloat16()
+        if heads_first:
+            k, v = k.transpose(1, 2), v.transpose(1, 2)
+        self.k, self.v = k, v
+        perm = torch.randperm(pool, generator=g, device="cuda").int()
+        width = width or max(count + [1]) + 1
+        tables = torch.full((len(count), width), 2 ** 30, dtype=torch.int32, device="cuda")
+        at = 0
+        used = torch.zeros(pool, dtype=torch.bool, device="cuda")
+        for i, c in enumerate(count):
+            tables[i, :c] = perm[at:at + c]
+            used[perm[at:at + c].long()] = True
+            n = max((lens + (prefix or []))[i], 0)
+            if poison and n % page:
+                k[perm[at + c - 1], n % page:] = math.nan
+                v[perm[at + c - 1], n % page:] = math.inf
+            at += c
+        if poison:
+            k[~used], v[~used] = math.nan, math.nan
+        n = len(lens)
+        self.table, self.far = tables[:n], tables[n:] if prefix else None
+        self.kv = paged.PagedKV(k, v)
+        self.batch = paged.PagedBatch(
+            self.table, ints(lens), None if q_lens is None else ints(q_lens), self.far,
+            ints(prefix) if prefix else None, ints(starts) if prefix else None)
+
+    def want(self, q, scale):
+        return ref.attention(q, self.k, self.v, self.table, self.lens, self.q_lens, self.far,
+                             self.prefix, self.starts, scale)
+
+    def check(self, q, got, lse=None, scale=None):
+        scale = scale if scale is not None else 1 / math.sqrt(q.shape[-1])
+        want, bound, want_lse, lse_bound = self.want(q, scale)
+        assert ref.close(got, want, bound, torch.bfloat16)
+        if lse is not None:
+            empty = want_lse == -math.inf
+            assert torch.equal(lse == -math.inf, empty)
+            off = (lse.double() - want_lse).abs()[~empty]
+            assert bool((off <= lse_bound[~empty]).all())
+        assert self.kv.device_error() == (0, 0)
+
+
+def bits(t):
+    return t.contiguous().view(torch.int16).clone()
+
+
+# ---- append -----------------------------------------------------------------
+
+APPEND = [  # lens, chunk, q_lens, kw
+    ([1], 1, None, {}),
+    ([700], 1, None, dict(kv_heads=8, dim=128)),
+    ([5, 16, 17, 33], 1, None, dict(page=8)),
+    ([40, 23, 64], 20, [20, 3, 0], dict(page=32, dim=80)),
+    ([3, 300, 12, 9, 1], 1, None, dict(prefix=[100, 7], starts=[1, 3, 4])),
+    ([66, 70], 66, [2, 66], dict(prefix=[1000], starts=[0, 2], heads_first=True, dim=128)),
+    ([2, 0, 5, 1], 3, [2, 0, 3, 1], dict(prefix=[0, 31, 5], starts=[0, 1, 1, 4], page=16)),
+    ([900, 1500], 700, [650, 700], dict(kv_heads=4, dim=256, page=128)),
+    ([1] * 64, 1, None, dict(prefix=[4096] * 40, starts=list(range(41)), kv_heads=1)),
+]
+
+
+@pytest.mark.parametrize("lens,chunk,q_lens,kw", APPEND)
+@pytest.mark.parametrize("tin,inter", [("f32", False), ("bf16", True)])
+def test_append(paged, lens, chunk, q_lens, kw, tin, inter):
+    c = Case(paged, len(lens) + chunk, lens, q_lens=q_lens, poison=False, **kw)
+    hk, dim = c.kv.kv_heads, c.kv.dim
+    h, rows = 3 * hk, len(lens) * chunk
+    y = randn(c.g, rows, (h + 2 * hk) * dim).to(DT[tin])
+    q, k, v = (t.unflatten(1, (-1, dim)) for t in y.split([h * dim, hk * dim, hk * dim], 1))
+    freq, kw_ = paged.rope_frequencies(dim // 2 // 8 * 8, 1e4), weights(c.g, "bf16", dim)
+    k0, v0 = c.k.clone(), c.v.clone()
+    got = c.kv.append(c.batch, k, v, q=q, freq=freq, q_weight=kw_, k_weight=kw_, interleaved=inter)
+    group = ref.groups_of(len(lens), c.starts)
+    pos, real, where = [], [], []
+    for b, n in enumerate(lens):
+        fresh = chunk if q_lens is None else q_lens[b]
+        base = c.prefix[group[b]] if group[b] is not None else 0
+        for i in range(chunk):
+            j = n - fresh + i
+            pos.append(base + j)
+            real.append(i < fresh)
+            if real[-1]:
+                where.append((b * chunk + i, int(c.table[b, j // c.kv.page_size]),
+                              j % c.kv.page_size))
+    pos, real = torch.tensor(pos, device="cuda"), torch.tensor(real, device="cuda")
+    want, bound = ref.norm_rotate(q, kw_, pos, freq, inter, 1e-6)
+    assert ref.close(got[real], want[real], bound[real], torch.bfloat16) and not got[~real].any()
+    want, bound = ref.norm_rotate(k, kw_, pos, freq, inter, 1e-6)
+    r, p, s = (torch.tensor(x, device="cuda") for x in zip(*where))
+    assert ref.close(c.k[p, s], want[r], bound[r], torch.bfloat16)
+    assert torch.equal(c.v[p, s], v[r].bfloat16())
+    c.k[p, s], c.v[p, s] = k0[p, s], v0[p, s]
+    assert torch.equal(bits(c.k), bits(k0)) and torch.equal(bits(c.v), bits(v0))
+    assert c.kv.device_error() == (0, 0)
+
+
+def test_append_without_q_or_rotation(paged):
+    c = Case(paged, 4, [4, 9], poison=False)
+    k, v = randn(c.g, 2, 2, 64), randn(c.g, 2, 2, 64)
+    assert c.kv.append(c.batch, k, v) is None
+    p, s = c.table[[0, 1], [0, 0]].long(), torch.tensor([3, 8], device="cuda")
+    assert torch.equal(c.k[p, s], k.bfloat16()) and torch.equal(c.v[p, s], v.bfloat16())
+
+
+def test_append_outside_the_tables(paged):
+    """Pages that are not there and lengths past the table: nothing is written."""
+    c = Case(paged, 5, [20, 20, 20, 20], poison=False, width=2)
+    c.table[0, 1], c.table[1, 1] = -1, c.k.shape[0]
+    lens = ints([20, 20, 33, 20])                      # the third's token is past its two pages
+    batch = paged.PagedBatch(c.table, lens)
+    k0, v0 = c.k.clone(), c.v.clone()
+    q, k, v = (randn(c.g, 4, 2, 64) for _ in range(3))
+    got = c.kv.append(batch, k, v, q=q)
+    assert torch.equal(got, q.bfloat16())
+    assert torch.equal(c.k[c.table[3, 1], 3], k[3].bfloat16())
+    c.k[c.table[3, 1], 3], c.v[c.table[3, 1], 3] = k0[c.table[3, 1], 3], v0[c.table[3, 1], 3]
+    assert torch.equal(bits(c.k), bits(k0)) and torch.equal(bits(c.v), bits(v0))
+    assert c.kv.device_error() == (1, 4) and c.kv.device_error() == (0, 0)
+    # A length of fewer than the new tokens leaves those before the start out.
+    c.kv.append(paged.PagedBatch(c.table, ints([0, -3, 0, 0])), k, v)
+    assert torch.equal(bits(c.k), bits(k0)) and c.kv.device_error() == (0, 0)
+
+
+# ---- attention --------------------------------------------------------------
+
+ATTEND = [  # lens, chunk, q_lens, heads, kw
+    ([1], 1, None, 2, {}),
+    ([127], 1, None, 8, dict(dim=128)),
+    ([128, 129, 255, 256, 257], 1, None, 4, {}),
+    ([1003], 1, None, 32, dict(kv_heads=8, dim=128)),
+    ([5000], 1, None, 8, dict(kv_heads=1, dim=128, page=8)),
+    ([0, 3, 0, 70], 1, None, 2, dict(page=8)),
+    ([0, 0], 1, None, 2, {}),
+    ([3, 300, 12, 9, 1], 1, None, 6, dict(prefix=[100, 700], starts=[1, 3, 4])),
+    ([1] * 8, 1, None, 32, dict(kv_heads=8, dim=128, prefix=[777], starts=[0, 8])),
+    ([7, 0, 20, 1], 1, None, 4, dict(prefix=[0, 31, 50], starts=[0, 1, 1, 4])),
+    ([9, 33, 2], 2, None, 4, dict(page=64)),
+    ([40, 23, 64], 20, [20, 3, 0], 2, dict(page=32, dim=128)),
+    ([66, 70], 66, [2, 66], 14, dict(prefix=[1000], starts=[0, 2], heads_first=True, dim=128)),
+    ([200], 200, None, 2, dict(page=16)),
+    ([700, 333], 150, [150, 77], 8, dict(page=256, prefix=[129, 5], starts=[0, 1, 2])),
+    ([17] * 64, 1, None, 8, dict(prefix=[2500], starts=[0, 64])),
+    ([17] * 64, 1, None, 32, dict(kv_heads=8, dim=128, prefix=[600], starts=[0, 64])),
+    ([4] * 70, 1, None, 16, dict(kv_heads=1, prefix=[300, 40], starts=[0, 68, 70])),
+    ([31] * 130, 1, None, 2, dict(prefix=[64] * 65, starts=list(range(0, 131, 2)))),
+    ([9] * 500, 1, None, 1, dict(kv_heads=1, prefix=[20, 20], starts=[0, 100, 400], page=8)),
+    ([2, 1, 3], 3, [2, 1, 3], 10, dict(prefix=[128], starts=[0, 3], dim=128)),
+    ([100, 20], 1, None, 128, dict(kv_heads=1, dim=128)),
+    ([300], 3, None, 256, dict(kv_heads=2, dim=64)),
+    ([20000], 64, None, 8, dict(kv_heads=2, dim=128, page=64)),
+]
+
+
+@pytest.mark.parametrize("lens,chunk,q_lens,heads,kw", ATTEND)
+def test_attend(paged, lens, chunk, q_lens, heads, kw):
+    c = Case(paged, len(lens) + heads, lens, q_lens=q_lens, **kw)
+    q = (2 * randn(c.g, len(lens) * chunk, heads, c.kv.dim)).bfloat16()
+    got, lse = c.kv.attend(c.batch, q, return_lse=True)
+    c.check(q, got, lse)
+    again = c.kv.attend(c.batch, q)
+    assert torch.equal(bits(got), bits(again))          # the same bits on every run
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
+def test_attend_scales(paged, scale):
+    """Uniform weights, turned signs, and scores of hundreds (one token takes all)."""
+    c = Case(paged, 6, [500, 40], dim=128, prefix=[900], starts=[0, 2])
+    q = (3 * randn(c.g, 2, 4, 128)).bfloat16()
+    got, lse = c.kv.attend(c.batch, q, scale=scale, return_lse=True)
+    c.check(q, got, lse, scale)
+
+
+def test_attend_rising_scores(paged):
+    """A running maximum that grows by more than any fixed step tile after tile."""
+    c = Case(paged, 7, [1500], kv_heads=1, dim=64, prefix=[1024], starts=[0, 1])
+    step = torch.linspace(0, 40, 1024, device="cuda").bfloat16()
+    flat = c.far[0, :64].long()
+    c.k[flat] = step.view(64, 16, 1, 1).expand(64, 16, 1, 64)
+    q = torch.full((1, 2, 64), 1.0, device="cuda").bfloat16()
+    q[0, 1] = -1
+    got, lse = c.kv.attend(c.batch, q, return_lse=True)
+    c.check(q, got, lse)
+
+
+def test_attend_infinite_keys(paged):
+    """Keys that make scores of -inf for some rows: such tokens weigh nothing; a
+    row with no other token is zero with an lse of -inf."""
+    c = Case(paged, 8, [300, 16], kv_heads=1, dim=64, poison=False)
+    q = torch.zeros((2, 1, 64), device="cuda").bfloat16()
+    q[..., 0] = 1
+    for b, n in ((0, 300), (1, 16)):
+        pages = c.table[b, :-(-n // 16)].long()
+        c.k[pages, :, :, 0] = 1.0
+    c.k[c.table[0, :10].long(), :, :, 0] = -math.inf
+    c.k[c.table[1, 0].long(), :, :, 0] = -math.inf
+    got, lse = c.kv.attend(c.batch, q, return_lse=True)
+    live = c.v[c.table[0, 10:19].long()].flatten(0, 1)[:140].double()
+    assert (got[0].double() - live.mean(0)).abs().max() <= 2.0 ** -7 * live.abs().max()
+    assert abs(float(lse[0, 0]) - (math.log(140) + 0.125)) < 1e-4
+    assert not got[1].any() and lse[1, 0] == -math.inf
+
+
+def test_attend_missing_pages(paged):
+    """A page outside the pool counts as zeros and is reported, tokens past the
+    table are not seen."""
+    c = Case(paged, 9, [64, 64], poison=False, width=4)
+    c.table[0, 2] = c.k.shape[0] + 5
+    q = randn(c.g, 2, 2, 64).bfloat16()
+    got = c.kv.attend(c.batch, q)
+    assert c.kv.device_error() == (1, 4)
+    k = torch.cat((c.k, torch.zeros_like(c.k[:1])))
+    v = torch.cat((c.v, torch.zeros_like(c.v[:1])))
+    table = c.table.clone()
+    table[0, 2] = c.k.shape[0]
+    want, bound, _, _ = ref.attention(q, k, v, table, [64, 64], None, None, None, None, 1 / 8)
+    assert ref.close(got, want, bound, torch.bfloat16)
+    over = paged.PagedBatch(c.table[1:], ints([90]))
+    got = c.kv.attend(over, q[1:])
+    assert c.kv.device_error() == (1, 4)
+    assert ref.close(got, want[1:], bound[1:], torch.bfloat16)
+
+
+def test_attend_strides(paged):
+    c = Case(paged, 10, [50, 7, 80], kv_heads=2, dim=64, heads_first=True)
+    q = randn(c.g, 4, 3, 128).bfloat16()[..., 64:].transpose(0, 1)     # heads outside tokens
+    store = torch.zeros((3, 5, 72), dtype=torch.bfloat16, device="cuda")
+    out = store[:, 1:, 8:]
+    assert c.kv.attend(c.batch, q, out=out) is out
+    c.check(q, out)
+    assert not store[:, 0].any() and not store[..., :8].any()
+
+
+def test_attend_far_offsets(paged):
+    """Pages whose offsets pass 2^32 elements."""
+    pages, page, hk, dim = 70000, 128, 8, 64
+    k = torch.empty((pages, page, hk, dim), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    assert k.numel() > 2 ** 32
+    g = gen(11)
+    ids = [pages - 1, 3, pages - 77, 65540]
+    for i in ids:
+        k[i], v[i] = randn(g, page, hk, dim).bfloat16(), randn(g, page, hk, dim).bfloat16()
+    kv = paged.PagedKV(k, v)
+    table = ints([ids])
+    batch = paged.PagedBatch(table, ints([400]))
+    new = [randn(g, 1, hk, dim) for _ in range(2)]
+    kv.append(batch, *new)
+    assert torch.equal(k[65540, 15], new[0][0].bfloat16())
+    assert torch.equal(v[65540, 15], new[1][0].bfloat16())
+    q = randn(g, 1, 16, dim).bfloat16()
+    got = kv.attend(batch, q)
+    want, bound, _, _ = ref.attention(q, k, v, table, [400], None, None, None, None, 1 / 8)
+    assert ref.close(got, want, bound, torch.bfloat16) and kv.device_error() == (0, 0)
+
+
+# ---- streams, graphs, the run of all three ------------------------------------
+
+def test_other_streams_at_once(paged):
+    """Two batches at once, on streams that are not the current one."""
+    cases = [Case(paged, 20 + i, [300 + i] * 12, dim=128, prefix=[3000], starts=[0, 12])
+             for i in range(2)]
+    qs = [randn(c.g, 12, 8, 128).bfloat16() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, c in enumerate(cases):
+            got[i].append(c.kv.attend(c.batch, qs[i], stream=streams[i]))
+    one = cases[0].kv.attend(cases[0].batch, qs[0], stream=streams[1].cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(bits(one), bits(got[0][0]))
+    for i, c in enumerate(cases):
+        for o in got[i]:
+            assert torch.equal(bits(o), bits(got[i][0]))
+        c.check(qs[i], got[i][0])
+
+
+def test_graph_replays_follow_lengths(paged):
+    """A captured append + attend replayed as the sequences grow; two graphs of
+    one cache keep their own workspace."""
+    g = gen(30)
+    pool = paged.PagedKV(randn(g, 40, 16, 2, 64).bfloat16(), randn(g, 40, 16, 2, 64).bfloat16())
+    table = torch.randperm(40, generator=g, device="cuda").int()[:37].contiguous()
+    own, far = table[:24].view(3, 8), table[24:].view(1, 13)
+    lens = ints([1, 20, 47])
+    batch = paged.PagedBatch(own, lens, prefix_table=far, prefix_lens=ints([200]),
+                             group_start=ints([0, 2]))
+    freq = paged.rope_frequencies(64, 1e4)
+    q, k, v = (randn(g, 3, n, 64) for n in (4, 2, 2))
+
+    def step():
+        qr = pool.append(batch, k, v, q=q, freq=freq)
+        return qr, pool.attend(batch, qr)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = step()
+        graphs.append((graph, outs))
+    now = [1, 20, 47]
+    for turn in range(30):
+        q.copy_(randn(g, 3, 4, 64)), k.copy_(randn(g, 3, 2, 64)), v.copy_(randn(g, 3, 2, 64))
+        graph, (qr, o) = graphs[turn % 2]
+        graph.replay()
+        want, bound, _, _ = ref.attention(qr, pool.k_pages, pool.v_pages, own, now, None, far,
+                                          [200], [0, 2], 1 / 8)
+        assert ref.close(o, want, bound, torch.bfloat16)
+        lens += 1
+        now = [n + 1 for n in now]
+    assert pool.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("batch_rows", [1, 3])
+def test_attention_block(paged, batch_rows):
+    """A layer's attention over compressed projections, token after token behind a
+    prompt taken in one chunk, against 64 bits from the same rounded inputs."""
+    from lossless_bf16_weight_nwc_b200 import _lib, synth
+    hidden, h, hk, dim, page = 256, 4, 2, 64, 16
+    w = [synth.matrix(synth.MatrixSpec("w", r, c, "normal", 0.06, 0), i)
+         for i, (r, c) in enumerate([(h * dim, hidden), (hk * dim, hidden), (hk * dim, hidden),
+                                     (hidden, h * dim)])]
+    wf = [torch.from_numpy(synth.bf16_bits_to_float(x).astype(np.float64)).cuda() for x in w]
+    g = gen(40)
+    kv = paged.PagedKV(*(randn(g, 24, page, hk, dim).bfloat16() for _ in range(2)))
+    qw, kw = weights(g, "bf16", dim), weights(g, "f32", dim).bfloat16()
+    freq = paged.rope_frequencies(dim, 5e5, factor=8.0)
+    block = paged.AttentionBlock(_lib.CompressedMatrix.compress_fused(w[:3]),
+                                 _lib.CompressedMatrix.compress(w[3]), kv, freq, qw, kw)
+    table = torch.arange(6 * batch_rows, device="cuda").int().view(batch_rows, 6)
+    lens = ints([0] * batch_rows)
+    batch = paged.PagedBatch(table, lens)
+    kept = [[], []]                                    # exact k and v of every token
+    at = 0
+    for chunk in (17, 1, 1, 1):
+        x = randn(g, batch_rows * chunk, hidden).bfloat16()
+        lens += chunk
+        y = block.step(x, batch)
+        pos = (at + torch.arange(chunk, device="cuda")).repeat(batch_rows)
+        q, k, v = ((x.double() @ m.T).unflatten(1, (-1, dim)) for m in wf[:3])
+        q = ref.norm_rotate(q, qw, pos, freq, False, 1e-6)[0].unflatten(0, (batch_rows, chunk))
+        k = ref.norm_rotate(k, kw, pos, freq, False, 1e-6)[0].unflatten(0, (batch_rows, chunk))
+        kept[0].append(k)
+        kept[1].append(v.unflatten(0, (batch_rows, chunk)))
+        ks, vs = (torch.cat(t, 1).repeat_interleave(h // hk, 2) for t in kept)
+        s = torch.einsum("bihd,bjhd->bhij", q, ks) / math.sqrt(dim)
+        i = at + torch.arange(chunk, device="cuda")
+        s = s.masked_fill(torch.arange(at + chunk, device="cuda") > i[:, None], -math.inf)
+        o = torch.einsum("bhij,bjhd->bihd", s.softmax(-1), vs)
+        want = o.flatten(2).flatten(0, 1) @ wf[3].T
+        # q, k, v, p and o are rounded to BF16 once each: 2^-8 at most, of which a
+        # score of size |s| takes 2 |s| 2^-8 into its weight.
+        top = float(torch.einsum("bihd,bjhd->bhij", q.abs(), ks.abs()).max() / math.sqrt(dim))
+        part = torch.einsum("bhij,bjhd->bihd", s.softmax(-1), vs.abs()).flatten(2).flatten(0, 1)
+        bound = (part @ wf[3].abs().T) * 2.0 ** -8 * (3 + 4 * top)
+        assert bool(((y.double() - want).abs() <= bound).all())
+        rel = float((y.double() - want).norm() / want.norm())
+        assert rel <= 2.0 ** -8 * (3 + 4 * top)
+        at += chunk
+    assert kv.device_error() == (0, 0)
