@@ -67,6 +67,32 @@ struct RopeParams {
 cudaError_t launch_rope(const RopeParams& p, int in_type, int out_type, int sm_count,
                         cudaStream_t stream);
 
+// Attention.  The work is cut into tiles of kKvTile tokens.  A segment is a
+// prefix with the rows of all its sequences, or a sequence's own tokens with its
+// rows; an item is a segment's rows of one key head, up to kPairRows of them;
+// the items' tiles lie end to end on one axis (segments, blocks of rows, key
+// heads, tiles), which the CTAs share out equally.  What a CTA does of an item is
+// a part; each of its two softmax teams leaves the part's running maximum, sum
+// and weighted values in the workspace, and a second kernel joins them.
+constexpr int kKvTile = 128;
+constexpr int kTeamRows = 128;
+constexpr int kPairRows = 2 * kTeamRows;
+
+// The workspace: where each segment's tiles and items start (segments + 1 each,
+// the last the totals), then the parts' results, prefixes' and own.
+struct AttentionWorkspace {
+  uint64_t starts;        // int64 [segments + 1]: first tile
+  uint64_t items;         // int32 [groups + 1]: first item of a prefix
+  uint64_t far_ml, far_o; // prefixes: float2 [slots][128], float [slots][128][dim]
+  uint64_t own_ml, own_o; // own: the same with own_rows rows
+  int64_t far_slots, own_slots;
+  int32_t own_rows;       // rows a slot of an own part holds
+  int32_t own_items;      // items of a sequence's own segment
+  uint64_t bytes;
+};
+AttentionWorkspace attention_workspace(int sequences, int chunk, int groups, int heads,
+                                       int kv_heads, int dim, int ctas);
+
 struct AttentionParams {
   HeadsView q, out;           // BF16 [rows][heads][dim]
   int32_t heads, kv_heads, dim;
@@ -74,11 +100,14 @@ struct AttentionParams {
   float* lse;                 // [rows][heads] or null
   CacheView cache;
   BatchView batch;
-  void* workspace;
+  uint8_t* workspace;
+  AttentionWorkspace ws;
+  int32_t ctas;
   uint32_t wait_limit;        // polls before a bounded wait gives up (0: default)
 };
-uint64_t attention_workspace(int sequences, int chunk, int groups, int heads, int kv_heads,
-                             int dim, int sm_count);
-cudaError_t launch_attention(const AttentionParams& p, int sm_count, cudaStream_t stream);
+// k_map, v_map: the pages as [pages][kv_heads][page_size][dim], box 64 elements
+// x min(page_size, 128) tokens, 128-byte swizzle.
+cudaError_t launch_attention(const AttentionParams& p, const CUtensorMap& k_map,
+                             const CUtensorMap& v_map, cudaStream_t stream);
 
 }  // namespace nwc

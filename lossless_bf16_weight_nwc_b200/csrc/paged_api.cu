@@ -126,6 +126,25 @@ nwc_status run_rope(const nwc::RopeParams& p, int in_type, int out_type, nwc_str
              : NWC_ERR_CUDA;
 }
 
+// The TMA descriptor of a cache's K or V pages.  Strides of dimensions of one
+// element play no part but have to be valid.
+bool page_map(const nwc_kv_cache& c, uint16_t* base, int64_t page_stride, int64_t token_stride,
+              int64_t head_stride, CUtensorMap* map) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nwc::tensor_map_encoder();
+  if (!encode) return false;
+  const int32_t rows = c.page_size < nwc::kKvTile ? c.page_size : nwc::kKvTile;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads,
+                              (cuuint64_t)c.pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)token_stride * 2, (cuuint64_t)head_stride * 2,
+                                 (cuuint64_t)page_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, elem,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool attention_shape(const nwc_kv_cache* c, const nwc_kv_batch* b, int32_t heads) {
   return good_cache(c) && good_batch(b) && heads >= 1 && heads <= kMaxHeads &&
          heads % c->kv_heads == 0;
@@ -190,7 +209,8 @@ nwc_status nwc_kv_attention_workspace(const nwc_kv_cache* cache, const nwc_kv_ba
   const nwc_status st = nwc::current_device(&dev, &sms, &smem);
   if (st != NWC_OK) return st;
   *bytes = nwc::attention_workspace(batch->sequences, batch->new_tokens, batch->groups, heads,
-                                    cache->kv_heads, cache->dim, sms);
+                                    cache->kv_heads, cache->dim, sms)
+               .bytes;
   return NWC_OK;
 }
 
@@ -201,27 +221,35 @@ nwc_status nwc_kv_attention(const nwc_kv_cache* cache, const nwc_kv_batch* batch
   if (!attention_shape(cache, batch, heads) || !wide_heads(q) || !wide_heads(out) ||
       !std::isfinite(scale) || !aligned_to(d_lse, 4))
     return NWC_ERR_INVALID_ARG;
-  uint64_t need = 0;
-  const nwc_status st = nwc_kv_attention_workspace(cache, batch, heads, &need);
-  if (st != NWC_OK) return st;
+  if (cache->dim != 64 && cache->dim != 128) return NWC_ERR_UNSUPPORTED;
   if (batch->sequences == 0) return NWC_OK;
-  if (!d_workspace || workspace_bytes < need || !aligned_to(d_workspace, 256))
-    return NWC_ERR_INVALID_ARG;
   int dev, sms;
   size_t smem;
-  const nwc_status sd = nwc::current_device(&dev, &sms, &smem);
-  if (sd != NWC_OK) return sd;
+  const nwc_status st = nwc::current_device(&dev, &sms, &smem);
+  if (st != NWC_OK) return st;
   nwc::AttentionParams p;
   std::memset(&p, 0, sizeof(p));
+  p.ctas = sms;
+  p.ws = nwc::attention_workspace(batch->sequences, batch->new_tokens, batch->groups, heads,
+                                  cache->kv_heads, cache->dim, sms);
+  if (!d_workspace || workspace_bytes < p.ws.bytes || !aligned_to(d_workspace, 256))
+    return NWC_ERR_INVALID_ARG;
   p.q = view(q), p.out = view(out);
   p.heads = heads, p.kv_heads = cache->kv_heads, p.dim = cache->dim;
   p.scale = scale;
   p.lse = d_lse;
   p.cache = view(*cache);
   p.batch = view(*batch);
-  p.workspace = d_workspace;
+  p.workspace = static_cast<uint8_t*>(d_workspace);
   p.wait_limit = nwc::wait_limit();
-  return nwc::launch_attention(p, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  CUtensorMap k_map, v_map;
+  if (!page_map(*cache, cache->d_k, cache->k_page_stride, cache->k_token_stride,
+                cache->k_head_stride, &k_map) ||
+      !page_map(*cache, cache->d_v, cache->v_page_stride, cache->v_token_stride,
+                cache->v_head_stride, &v_map))
+    return NWC_ERR_UNSUPPORTED;
+  return nwc::launch_attention(p, k_map, v_map, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
              ? NWC_OK
              : NWC_ERR_CUDA;
 }

@@ -26,6 +26,10 @@ from . import _lib
 
 _TYPES = {torch.bfloat16: _lib.NWC_TYPE_BF16, torch.float32: _lib.NWC_TYPE_F32}
 _HEADS = ctypes.sizeof(_lib.nwc_heads)
+_ROPE = ctypes.sizeof(_lib.nwc_rope)
+_POSITIONS = (torch.int32, torch.int64)
+_BF16 = (torch.bfloat16,)
+_F64 = (torch.float64,)
 
 
 def rope_frequencies(rotary_dim: int, theta: float = 10000.0, device="cuda",
@@ -46,9 +50,11 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, device="cuda",
 
 
 def _no_grad(*tensors) -> None:
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError("an input requires a gradient, which these kernels do not give; "
-                         "call under torch.no_grad()")
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("an input requires a gradient, which these kernels do not "
+                                 "give; call under torch.no_grad()")
 
 
 def _heads(t, what: str, shape, device, dtypes=_TYPES):
@@ -56,17 +62,18 @@ def _heads(t, what: str, shape, device, dtypes=_TYPES):
     contiguous last dimension."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{what}: dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
+    dtype = t.dtype
+    if dtype not in dtypes:
+        raise TypeError(f"{what}: dtype {dtype}, expected one of {[str(d) for d in dtypes]}")
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    st = t.stride()
-    if st[2] != 1:
+    ts, hs, es = t.stride()
+    if es != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
     if t.device != device:
         raise ValueError(f"{what}: on {t.device}, expected {device}")
-    return _lib.nwc_heads(_HEADS, _TYPES[t.dtype], t.data_ptr(), st[0] if shape[0] > 1 else 0,
-                          st[1] if shape[1] > 1 else 0)
+    return _lib.nwc_heads(_HEADS, _TYPES[dtype], t.data_ptr(), ts if shape[0] > 1 else 0,
+                          hs if shape[1] > 1 else 0)
 
 
 def _output(t, what: str, shape, device, dtypes):
@@ -77,6 +84,13 @@ def _output(t, what: str, shape, device, dtypes):
             (heads == 1 or rows == 1 or ts >= heads * hs or hs >= rows * ts)) and rows:
         raise ValueError(f"{what}: its elements overlap")
     return h
+
+
+def _new(shape, device):
+    """A new BF16 tensor [tokens, heads, dim] and its C view."""
+    t = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    dim = shape[2]
+    return t, _lib.nwc_heads(_HEADS, _lib.NWC_TYPE_BF16, t.data_ptr(), shape[1] * dim, dim)
 
 
 def _vector(t, what: str, device, n: int, dtypes) -> int:
@@ -93,43 +107,75 @@ def _vector(t, what: str, device, n: int, dtypes) -> int:
 
 
 def _rope(dim: int, device, freq, q_weight, k_weight, eps: float, interleaved: bool):
-    r = _lib.nwc_rope(ctypes.sizeof(_lib.nwc_rope), 0, interleaved, 0, None, None, None, eps)
     if not 0 <= eps < math.inf:
         raise ValueError("eps: a finite number, not negative")
+    n, d_freq, d_q, d_k, kind = 0, None, None, None, 0
     if freq is not None:
         n = freq.numel() if isinstance(freq, torch.Tensor) else 0
-        r.d_freq = _vector(freq, "freq", device, n, (torch.float64,))
+        d_freq = _vector(freq, "freq", device, n, _F64)
         if 2 * n > dim or n % 4:
             raise ValueError(f"freq: {n} elements; a multiple of 4 up to {dim // 2}")
-        r.rotary_dim = 2 * n
-    types = {w.dtype for w in (q_weight, k_weight) if isinstance(w, torch.Tensor)}
-    if len(types) > 1:
-        raise TypeError("q_weight and k_weight: expected one dtype")
     if q_weight is not None:
-        r.d_q_weight = _vector(q_weight, "q_weight", device, dim, _TYPES)
+        d_q = _vector(q_weight, "q_weight", device, dim, _TYPES)
+        kind = _TYPES[q_weight.dtype]
     if k_weight is not None:
-        r.d_k_weight = _vector(k_weight, "k_weight", device, dim, _TYPES)
-    if types:
-        r.weight_type = _TYPES[types.pop()]
-    return r
+        if q_weight is not None and k_weight.dtype != q_weight.dtype:
+            raise TypeError("q_weight and k_weight: expected one dtype")
+        d_k = _vector(k_weight, "k_weight", device, dim, _TYPES)
+        kind = _TYPES[k_weight.dtype]
+    return _lib.nwc_rope(_ROPE, 2 * n, interleaved, kind, d_freq, d_q, d_k, eps)
 
 
-def _on(device, stream, call):
-    """call() with the device current and, when a stream is given, that stream
-    current too: what the call allocates then belongs to the stream it runs on."""
-    if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return call()
-        with torch.cuda.device(device):
-            return call()
-    if not isinstance(stream, torch.cuda.Stream):
-        raw = int(getattr(stream, "cuda_stream", stream))
-        stream = (torch.cuda.ExternalStream(raw, device=device) if raw
-                  else torch.cuda.default_stream(device))
-    if stream.device != device:
-        raise ValueError(f"stream: on {stream.device}, expected {device}")
-    with torch.cuda.stream(stream):
-        return call()
+class _On:
+    """Makes a call's device current and, when a stream is given, that stream
+    current too: what the call allocates then belongs to the stream it runs on.
+    Entering gives the stream's handle."""
+
+    def __init__(self, device, stream):
+        if stream is None:
+            self.context = torch.cuda.device(device)
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                raw = int(getattr(stream, "cuda_stream", stream))
+                stream = (torch.cuda.ExternalStream(raw, device=device) if raw
+                          else torch.cuda.default_stream(device))
+            if stream.device != device:
+                raise ValueError(f"stream: on {stream.device}, expected {device}")
+            self.context = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.context.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *args):
+        return self.context.__exit__(*args)
+
+
+class _Here:
+    """_On for the current device's current stream, which needs no switch."""
+
+    def __init__(self, raw: int):
+        self.raw = raw
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *args):
+        return None
+
+
+def _on(device, stream):
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _Here(_raw_stream(device.index))
+    return _On(device, stream)
+
+
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The same handle without building a torch.cuda.Stream (3 us less a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _cuda(t, what: str):
@@ -152,42 +198,42 @@ def qk_norm_rope(q, k, positions, freq=None, q_weight=None, k_weight=None, eps: 
     themselves) holds."""
     first = q if q is not None else k
     device = _cuda(first, "q" if q is not None else "k")
-    _no_grad(q, k, q_weight, k_weight, freq)
+    _no_grad(q, k, q_weight, k_weight)
     if first.dim() != 3:
         raise ValueError("q, k: expected [tokens, heads, dim]")
-    tokens, _, dim = first.shape
-    pair = []
-    for t, what in ((q, "q"), (k, "k")):
-        if t is None:
-            pair.append((0, None))
-            continue
-        if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            raise ValueError(f"{what}: expected a tensor [tokens, heads, dim]")
-        pair.append((t.shape[1], _heads(t, what, (tokens, t.shape[1], dim), device)))
-    if q is not None and k is not None and q.dtype != k.dtype:
-        raise TypeError("q and k: expected one dtype")
+    tokens, heads, dim = first.shape
     if not 8 <= dim <= 256 or dim % 8:
         raise ValueError(f"dim {dim}: a multiple of 8 from 8 to 256")
+    qh = None if q is None else _heads(q, "q", (tokens, heads, dim), device)
+    kh, kv_heads = None, heads
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("k: expected a tensor [tokens, heads, dim]")
+        kv_heads = k.shape[1]
+        kh = _heads(k, "k", (tokens, kv_heads, dim), device, (first.dtype,))
     rope = _rope(dim, device, freq, q_weight, k_weight, eps, interleaved)
-    at = _vector(positions, "positions", device, tokens, (torch.int32, torch.int64))
-    if out is not None and (len(out) != 2 or any((o is None) != (t is None)
-                                                 for o, t in zip(out, (q, k)))):
-        raise ValueError("out: a pair of tensors for q and k, None where the input is None")
-
-    def call():
-        res = out if out is not None else [
-            None if t is None else torch.empty(t.shape, dtype=torch.bfloat16, device=device)
-            for t in (q, k)]
-        to = [None if o is None else _output(o, f"{w}_out", t.shape, device, _TYPES)
-              for o, t, w in zip(res, (q, k), "qk")]
-        if to[0] is not None and to[1] is not None and to[0].type != to[1].type:
-            raise TypeError("out: expected one dtype")
+    at = _vector(positions, "positions", device, tokens, _POSITIONS)
+    with _on(device, stream) as raw:
+        qo = ko = qoh = koh = None
+        if out is None:
+            if q is not None:
+                qo, qoh = _new((tokens, heads, dim), device)
+            if k is not None:
+                ko, koh = _new((tokens, kv_heads, dim), device)
+        else:
+            qo, ko = out
+            if (qo is None) != (q is None) or (ko is None) != (k is None):
+                raise ValueError("out: a pair of tensors for q and k, None where the input is "
+                                 "None")
+            if q is not None:
+                qoh = _output(qo, "out[0]", (tokens, heads, dim), device, _TYPES)
+            if k is not None:
+                koh = _output(ko, "out[1]", (tokens, kv_heads, dim), device,
+                              _TYPES if q is None else (qo.dtype,))
         if tokens:
-            _lib.nwc_qk_norm_rope(pair[0][1], pair[1][1], to[0], to[1], tokens, pair[0][0],
-                                  pair[1][0], dim, at, positions.dtype == torch.int64, rope)
-        return tuple(res)
-
-    return _on(device, stream, call)
+            _lib.nwc_qk_norm_rope(qh, kh, qoh, koh, tokens, heads, kv_heads, dim, at,
+                                  positions.dtype == torch.int64, rope, raw)
+    return qo, ko
 
 
 class PagedBatch:
@@ -325,32 +371,30 @@ class PagedKV:
         seq_lens counts the new tokens already.  Padding rows are not appended,
         their q is zero."""
         rows, view = self._rows(batch, k, "k")
-        _no_grad(q, k, v, q_weight, k_weight, freq)
+        _no_grad(q, k, v, q_weight, k_weight)
         device = self.device
-        kh = _heads(k, "k", (rows, self.kv_heads, self.dim), device)
-        vh = _heads(v, "v", (rows, self.kv_heads, self.dim), device, (k.dtype,))
-        if q is None:
-            if q_out is not None:
-                raise ValueError("q_out: given without q")
-            heads, qh = 1, None
-        else:
+        shape = (rows, self.kv_heads, self.dim)
+        kh = _heads(k, "k", shape, device)
+        same = (k.dtype,)
+        vh = _heads(v, "v", shape, device, same)
+        heads, qh, qoh = 1, None, None
+        if q is not None:
             if not isinstance(q, torch.Tensor) or q.dim() != 3:
                 raise ValueError("q: expected a tensor [rows, heads, dim]")
             heads = q.shape[1]
-            qh = _heads(q, "q", (rows, heads, self.dim), device, (k.dtype,))
+            shape = (rows, heads, self.dim)
+            qh = _heads(q, "q", shape, device, same)
+        elif q_out is not None:
+            raise ValueError("q_out: given without q")
         rope = _rope(self.dim, device, freq, q_weight, k_weight, eps, interleaved)
-
-        def call():
-            out = q_out
-            if q is not None and out is None:
-                out = torch.empty((rows, heads, self.dim), dtype=torch.bfloat16, device=device)
-            oh = None if out is None else _output(out, "q_out", (rows, heads, self.dim), device,
-                                                  (torch.bfloat16,))
+        with _on(device, stream) as raw:
+            if q_out is not None:
+                qoh = _output(q_out, "q_out", shape, device, _BF16)
+            elif q is not None:
+                q_out, qoh = _new(shape, device)
             if rows:
-                _lib.nwc_kv_append(self._view, view, qh, oh, heads, kh, vh, rope)
-            return out
-
-        return _on(device, stream, call)
+                _lib.nwc_kv_append(self._view, view, qh, qoh, heads, kh, vh, rope, raw)
+        return q_out
 
     def attend(self, batch: PagedBatch, q, scale: float | None = None, out=None,
                return_lse: bool = False, stream=None):
@@ -366,17 +410,17 @@ class PagedKV:
         heads = q.shape[1]
         if heads < 1 or heads % self.kv_heads:
             raise ValueError(f"q: {heads} heads, expected a multiple of {self.kv_heads}")
-        bf16 = (torch.bfloat16,)
-        qh = _heads(q, "q", (rows, heads, self.dim), self.device, bf16)
-        if qh.d_data and (qh.d_data % 16 or qh.token_stride % 8 or qh.head_stride % 8):
+        shape = (rows, heads, self.dim)
+        qh = _heads(q, "q", shape, self.device, _BF16)
+        if rows and (qh.d_data % 16 or qh.token_stride % 8 or qh.head_stride % 8):
             raise ValueError("q: needs 16-byte alignment and strides of multiples of 8 elements")
         if scale is None:
-            scale = 1.0 / math.sqrt(self.dim)
-
-        def call():
-            o = torch.empty((rows, heads, self.dim), dtype=torch.bfloat16,
-                            device=self.device) if out is None else out
-            oh = _output(o, "out", (rows, heads, self.dim), self.device, bf16)
+            scale = self.dim ** -0.5
+        with _on(self.device, stream) as raw:
+            if out is None:
+                out, oh = _new(shape, self.device)
+            else:
+                oh = _output(out, "out", shape, self.device, _BF16)
             lse = torch.empty((rows, heads), dtype=torch.float32,
                               device=self.device) if return_lse else None
             if rows:
@@ -388,10 +432,8 @@ class PagedKV:
                 # From torch's allocator on the call's stream: calls on different
                 # streams, and captured graphs, each have their own.
                 ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-                _lib.nwc_kv_attention(self._view, view, qh, heads, scale, oh, lse, ws, need)
-            return (o, lse) if return_lse else o
-
-        return _on(self.device, stream, call)
+                _lib.nwc_kv_attention(self._view, view, qh, heads, scale, oh, lse, ws, need, raw)
+        return (out, lse) if return_lse else out
 
 
 class AttentionBlock:
