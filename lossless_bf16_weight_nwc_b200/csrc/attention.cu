@@ -57,11 +57,11 @@ static_assert(Layout<64>::kRing <= kMaxRing && Layout<128>::kBytes <= 232448, "s
 
 struct Bars {
   uint64_t full[kMaxRing];   // a tile's bytes landed
-  uint64_t empty[kMaxRing];  // the products that read the tile are done
+  uint64_t empty[kMaxRing];  // the products that read the tile are done (2 arrivals)
   uint64_t qfull[2];         // the team's Q is in place
-  uint64_t sfull[2];         // the team's S is in TMEM
+  uint64_t sfull[2];         // the team's S is in TMEM (and its P V before that is done)
   uint64_t pfull[2];         // the team's P is in TMEM (and V's tail is zeroed)
-  uint64_t ofull[2];         // the team's P V is done
+  uint64_t ofull[2];         // the last P V of the team's part is done
   uint64_t drain;
   uint32_t tmem;
   uint32_t abort;
@@ -258,36 +258,49 @@ __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* k_map,
 struct Unit {
   uint32_t tile;   // of the CTA
   bool first;      // the team's first of a part
-  bool last_use;   // of the tile
+  bool last;       // the team's last of a part
 };
 struct Units {
   Walk walk;
-  Part part;
   uint32_t tile = 0, team = 0;
   int left = 0, begun = 0;  // uses left of the part, teams that have begun it (bits)
+  bool both = false;
+  int next_n = 0;           // tiles of the part after it, 0: none
+  bool next_both = false;
+  __device__ __forceinline__ void look_ahead(const AttentionParams& p) {
+    Part part;
+    next_n = walk.next(p, part) ? part.n : 0;
+    next_both = part.both;
+  }
   __device__ __forceinline__ bool next(const AttentionParams& p, Unit& u, uint32_t& team_out) {
     if (left == 0) {
-      if (!walk.next(p, part)) return false;
-      left = part.both ? 2 * part.n : part.n;
+      if (next_n == 0) return false;
+      both = next_both;
+      left = both ? 2 * next_n : next_n;
       begun = 0;
+      look_ahead(p);
     }
     team_out = team;
     u.tile = tile;
     u.first = !(begun >> team & 1);
     begun |= 1 << team;
     --left;
-    u.last_use = !part.both || (left & 1) == 0;
-    if (u.last_use) ++tile;
+    u.last = left < 2;
+    if (!both || (left & 1) == 0) ++tile;
     team ^= 1;
     return true;
   }
 };
 
-// Issues every product of the CTA (one thread).
+// Issues every product of the CTA (a whole warp, its first lane in effect).  A
+// commit costs the issuer about as much as two products, so there is one a unit:
+// it follows a team's P V and the S of its next unit, and the team passes the
+// tiles it has then done with back to the producer.
 template <int DIM>
 __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* bars, Walk walk,
                                const Ctl& ctl) {
   using L = Layout<DIM>;
+  const uint32_t leader = (threadIdx.x & 31) == 0;
   const uint32_t tmem = bars->tmem;
   const uint32_t ring = smem_u32(smem + L::kRingOff), q = smem_u32(smem + L::kQOff);
   constexpr uint32_t id_s = umma_idesc_bf16(kTeamRows, kKvTile);
@@ -295,20 +308,21 @@ __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* ba
   uint32_t q_turn[2] = {0, 0}, p_turn[2] = {0, 0};
   Units units;
   units.walk = walk;
+  units.look_ahead(p);
 
   auto issue_s = [&](const Unit& u, uint32_t w) -> bool {
     if (u.first && !wait(&bars->qfull[w], q_turn[w]++ & 1u, ctl)) return false;
     const uint32_t seq = 2 * u.tile, slot = seq % L::kRing;
     if (!wait(&bars->full[slot], (seq / L::kRing) & 1u, ctl)) return false;
     tc_fence_after();
-    const uint32_t a = q + w * L::kTile, b = ring + slot * L::kTile;
+    const uint64_t a = umma_desc_sw128(q + w * L::kTile);
+    const uint64_t b = umma_desc_sw128(ring + slot * L::kTile);
 #pragma unroll
     for (int k = 0; k < DIM / 16; ++k) {
-      const uint32_t off = (uint32_t)(k / 4) * (kKvTile * 128u) + (uint32_t)(k % 4) * 32u;
-      umma_bf16(tmem + w * 128u, umma_desc_sw128(a + off), umma_desc_sw128(b + off), id_s, k > 0);
+      const uint32_t off = ((uint32_t)(k / 4) * (kKvTile * 128u) + (uint32_t)(k % 4) * 32u) >> 4;
+      umma_bf16_by(leader, tmem + w * 128u, a + off, b + off, id_s, k > 0);
     }
-    umma_commit(&bars->sfull[w]);
-    if (u.last_use) umma_commit(&bars->empty[slot]);
+    umma_commit_by(leader, &bars->sfull[w]);
     return true;
   };
   auto issue_o = [&](const Unit& u, uint32_t w) -> bool {
@@ -316,14 +330,12 @@ __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* ba
     const uint32_t seq = 2 * u.tile + 1, slot = seq % L::kRing;
     if (!wait(&bars->full[slot], (seq / L::kRing) & 1u, ctl)) return false;
     tc_fence_after();
-    const uint32_t b = ring + slot * L::kTile;
+    const uint64_t b = umma_desc_mn_sw128(ring + slot * L::kTile, kKvTile * 128u);
 #pragma unroll
     for (int k = 0; k < kKvTile / 16; ++k)
-      umma_bf16_ts(tmem + 256u + w * 128u, tmem + w * 128u + 8u * k,
-                   umma_desc_mn_sw128(b + (uint32_t)k * 2048u, kKvTile * 128u), id_o,
-                   !u.first || k > 0);
-    umma_commit(&bars->ofull[w]);
-    if (u.last_use) umma_commit(&bars->empty[slot]);
+      umma_bf16_ts_by(leader, tmem + 256u + w * 128u, tmem + w * 128u + 8u * k,
+                      b + ((uint32_t)k * 2048u >> 4), id_o, !u.first || k > 0);
+    if (u.last) umma_commit_by(leader, &bars->ofull[w]);
     return true;
   };
 
@@ -337,7 +349,7 @@ __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* ba
     a = b, wa = wb, has_a = has_b;
     b = c, wb = wc, has_b = has_c;
   }
-  umma_commit(&bars->drain);
+  umma_commit_by(leader, &bars->drain);
   wait_bounded(&bars->drain, 0, drain_ctl_default(p.cache.err));
 }
 
@@ -349,6 +361,32 @@ __device__ __forceinline__ float exp2_approx(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Two probabilities (not negative) to BF16, to nearest with ties up: adds and a
+// byte permute, as the conversion instruction shares the exponential's unit,
+// which bounds the softmax.  A NaN is lost here but not in the row's sum, which
+// every value of the row is divided by.
+__device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo) + 0x8000u, __float_as_uint(hi) + 0x8000u, 0x7632);
 }
 
 // A softmax team: thread r has row r of the team's rows.
@@ -368,104 +406,142 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
   const float c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-38f);
   const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
   uint32_t turn = 0;       // this team's uses of tiles so far
+  uint32_t done = 0;       // and its parts with at least one
   uint32_t uses = 0;       // both teams' uses so far
   uint32_t tiles = 0;      // tiles of the CTA so far
   Part part;
-  while (walk.next(p, part)) {
-    // This thread's row: which token and query head, and how many of the
-    // segment's tokens it sees.
+  bool more = walk.next(p, part);
+  while (more) {
+    // This thread's row: how many of the segment's tokens it sees.
     const int base = part.block * kPairRows + (part.both ? (int)w * kTeamRows : 0);
     const int team_rows = min(part.seg.rows - base, kTeamRows);
     const int first = part.both ? 0 : (int)((uses ^ w) & 1u);    // the team's first tile
     const int step = part.both ? 1 : 2;
+    const int last = first + (part.n - 1 - first) / step * step;  // (when first < part.n)
     const bool zeroes = !part.both || w == (uses & 1u);          // the tile's first user
-    int limit = 0, token = 0, head = 0;
-    if (r < team_rows) {
-      const int per = b.chunk * gq, row = base + r;
-      const int sl = row / per, rest = row - sl * per, i = rest / gq;
-      const int seq = part.seg.seq0 + sl, fresh = fresh_of(b, seq);
-      token = seq * b.chunk + i;
-      head = part.kvh * gq + rest - i * gq;
-      if (i < fresh)
-        limit = part.seg.far ? part.seg.len
-                             : min(max(max(b.lens[seq], 0) - fresh + i + 1, 0), part.seg.len);
-    }
-    float m = -INFINITY, l = 0.f;
-    if (first < part.n) {
-      // Q's row into the team's buffer: 16-byte pieces, 128-byte swizzle.
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const uint16_t*>(p.q.data) + (int64_t)token * p.q.token_stride +
-          (int64_t)head * p.q.head_stride);
-      const uint32_t dst = smem_u32(smem + L::kQOff + w * L::kTile) + (uint32_t)r * 128u;
-#pragma unroll
-      for (int k = 0; k < DIM / 8; ++k) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (limit > 0) v = src[k];
-        sts128(dst + (uint32_t)(k / 8) * (kTeamRows * 128u) + (uint32_t)((k % 8) ^ (r & 7)) * 16u,
-               v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+    const bool begins = first < part.n;
+    const int per = b.chunk * gq;
+    if (begins) {
+      // Q's rows into the team's buffer: 16-byte pieces, 128-byte swizzle.  Rows
+      // behind the last keep what is there: no row's result meets another's.
+      constexpr int kPieces = DIM / 8, kStep = kTeamThreads / kPieces;
+      const int piece = r % kPieces;
+      const uint32_t dst = smem_u32(smem + L::kQOff + w * L::kTile) +
+                           (uint32_t)(piece / 8) * (kTeamRows * 128u);
+#pragma unroll 4
+      for (int row = r / kPieces; row < team_rows; row += kStep) {
+        const int sl = (base + row) / per, rest = base + row - sl * per, i = rest / gq;
+        const uint4 v = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q.data) +
+            (int64_t)((part.seg.seq0 + sl) * b.chunk + i) * p.q.token_stride +
+            (int64_t)(part.kvh * gq + rest - i * gq) * p.q.head_stride)[piece];
+        sts128(dst + (uint32_t)row * 128u + (uint32_t)((piece % 8) ^ (row & 7)) * 16u, v.x ^ flip,
+               v.y ^ flip, v.z ^ flip, v.w ^ flip);
       }
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(&bars->qfull[w]);
     }
+    int limit = 0;
+    if (r < team_rows) {
+      const int sl = (base + r) / per, i = (base + r - sl * per) / gq;
+      const int seq = part.seg.seq0 + sl, fresh = fresh_of(b, seq);
+      if (i < fresh)
+        limit = part.seg.far ? part.seg.len
+                             : min(max(max(b.lens[seq], 0) - fresh + i + 1, 0), part.seg.len);
+    }
+    Part next;
+    more = walk.next(p, next);   // while the first scores are on their way
+    float m = -INFINITY, l = 0.f;
     const bool warp_live = __any_sync(kAll, limit > 0);
     for (int t = first; t < part.n; t += step, ++turn) {
       const int t0 = (part.tile0 + t) * kKvTile;
       if (!__all_sync(kAll, wait(&bars->sfull[w], turn & 1u, ctl))) return;
       tc_fence_after();
+      if (r == 0) {   // S is there: K has been read, and the V of the unit before
+        mbar_arrive_n(&bars->empty[2 * (tiles + (uint32_t)t) % L::kRing], part.both ? 1 : 2);
+        if (t != first)
+          mbar_arrive_n(&bars->empty[(2 * (tiles + (uint32_t)(t - step)) + 1) % L::kRing],
+                        part.both ? 1 : 2);
+      }
       if (warp_live) {
-        const int cols = limit - t0;
-        float s[kKvTile];
+        // Rows that are not there need no mask: nothing of theirs is read.
+        const int cols = r < team_rows ? limit - t0 : kKvTile;
+        const bool tail = __any_sync(kAll, cols < kKvTile);
+        // The maximum first, then the scores once more for the exponentials, in
+        // rolled halves: as straight code the two passes do not fit the
+        // instruction cache, which cost a lone warp twice the time.
+        float top[4] = {m, m, m, m};
+#pragma unroll 1
+        for (int h = 0; h < kKvTile; h += 64) {
+          float x[64];
+          tmem_load32(ts + (uint32_t)h, x);
+          tmem_load32(ts + (uint32_t)h + 32u, x + 32);
+          tmem_wait_load();
+          tmem_tie<64>(x);
+          if (tail) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_load32(ts + 32u * k, s + 32 * k);
-        tmem_wait_load();
-        tmem_tie<kKvTile>(s);
-        if (__any_sync(kAll, cols < kKvTile)) {
+            for (int j = 0; j < 64; ++j) x[j] = j < cols - h ? x[j] : -INFINITY;
+          }
 #pragma unroll
-          for (int j = 0; j < kKvTile; ++j) s[j] = j < cols ? s[j] : -INFINITY;
+          for (int j = 0; j < 64; j += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[j + k]), x[j + k + 4]);
         }
-        float top[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top[k] = s[k];
-#pragma unroll
-        for (int j = 4; j < kKvTile; ++j) top[j & 3] = fmaxf(top[j & 3], s[j]);
-        const float now = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
+        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         const bool grow = now > m && !((now - m) * c <= kLazy);
         if (__any_sync(kAll, grow)) {
           const float keep = m == -INFINITY ? 0.f : exp2_approx((m - now) * c);
           const float f = grow ? keep : 1.f;
           if (t != first) {
-            if (!__all_sync(kAll, wait(&bars->ofull[w], (turn - 1) & 1u, ctl))) return;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < DIM / 16; ++k) {
+#pragma unroll 1
+            for (int k = 0; k < DIM; k += 16) {
               float o[16];
-              tmem_load<16>(to + 16u * k, o);
+              tmem_load<16>(to + (uint32_t)k, o);
               uint32_t u[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * f);
-              tmem_store16(to + 16u * k, u);
+              tmem_store16(to + (uint32_t)k, u);
             }
           }
           l *= f;
           if (grow) m = now;
         }
         const float shift = m == -INFINITY ? 0.f : m * c;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t c2 = pack_f32x2(c, c), shift2 = pack_f32x2(-shift, -shift);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+        for (int h = 0; h < kKvTile; h += 64) {
+          float x[64];
+          tmem_load32(ts + (uint32_t)h, x);
+          tmem_load32(ts + (uint32_t)h + 32u, x + 32);
+          tmem_wait_load();
+          tmem_tie<64>(x);
+          if (tail) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t u[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float a = exp2_approx(fmaf(s[32 * k + 2 * j], c, -shift));
-            const float d = exp2_approx(fmaf(s[32 * k + 2 * j + 1], c, -shift));
-            sum[j & 1] += a;
-            sum[2 + (j & 1)] += d;
-            u[j] = pack_bf16(a, d);
+            for (int j = 0; j < 64; ++j) x[j] = j < cols - h ? x[j] : -INFINITY;
           }
-          tmem_store16(ts + 16u * k, u);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t u[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float a, d;
+              unpack_f32x2(
+                  fma_f32x2(pack_f32x2(x[32 * k + 2 * j], x[32 * k + 2 * j + 1]), c2, shift2), a,
+                  d);
+              a = exp2_approx(a);
+              d = exp2_approx(d);
+              sum[j & 1] = add_f32x2(sum[j & 1], pack_f32x2(a, d));
+              u[j] = round_bf16x2(a, d);
+            }
+            // P over S: columns h / 2 .. h / 2 + 31, whose scores have been read.
+            tmem_store16(ts + (uint32_t)h / 2 + 16u * k, u);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float s0, s1;
+        unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
         tmem_wait_store();
       }
       // Tokens behind the segment's last: whatever the pages hold there, V is zero.
@@ -488,26 +564,30 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
     const int64_t slot = slot_of(p, part.s, part.item, (int)blockIdx.x, (int)w);
     const int slot_rows = part.seg.far ? kTeamRows : p.ws.own_rows;
     const bool room = slot < (part.seg.far ? p.ws.far_slots : p.ws.own_slots);
+    const bool writes = r < team_rows && room;
     float* o_at = reinterpret_cast<float*>(p.workspace +
                                            (part.seg.far ? p.ws.far_o : p.ws.own_o)) +
                   (slot * slot_rows + r) * DIM;
-    if (r < team_rows && room)
+    if (writes)
       reinterpret_cast<float2*>(p.workspace + (part.seg.far ? p.ws.far_ml : p.ws.own_ml))
           [slot * slot_rows + r] = make_float2(m * c, l);
-    if (first < part.n) {
-      if (!__all_sync(kAll, wait(&bars->ofull[w], (turn - 1) & 1u, ctl))) return;
+    if (begins) {
+      if (!__all_sync(kAll, wait(&bars->ofull[w], done++ & 1u, ctl))) return;
       tc_fence_after();
+      if (r == 0)
+        mbar_arrive_n(&bars->empty[(2 * (tiles + (uint32_t)last) + 1) % L::kRing],
+                      part.both ? 1 : 2);
       if (warp_live) {
-#pragma unroll
-        for (int k = 0; k < DIM / 32; ++k) {
+#pragma unroll 1
+        for (int k = 0; k < DIM; k += 32) {
           float o[32];
-          tmem_load32(to + 32u * k, o);
+          tmem_load32(to + (uint32_t)k, o);
           tmem_wait_load();
           tmem_tie<32>(o);
-          if (r < team_rows && room) {
+          if (writes) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              reinterpret_cast<float4*>(o_at + 32 * k)[j] =
+              reinterpret_cast<float4*>(o_at + k)[j] =
                   make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
@@ -517,6 +597,7 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
     if (!room && r == 0) atomicOr(p.cache.err, kErrRange);
     uses += (uint32_t)(part.both ? 2 * part.n : part.n);
     tiles += (uint32_t)part.n;
+    part = next;
   }
 }
 
@@ -627,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int k = 0; k < L::kRing; ++k) {
       mbar_init(&bars->full[k], 1);
-      mbar_init(&bars->empty[k], 1);
+      mbar_init(&bars->empty[k], 2);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bars->qfull[w], kTeamThreads);
@@ -654,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     softmax_team<DIM>(p, smem, bars, walk, ctl, (uint32_t)(warp >> 2));
   } else if (warp == kProducerWarp) {
     produce_kv<DIM>(p, &k_map, &v_map, smem, bars, walk, ctl);
-  } else if ((threadIdx.x & 31) == 0) {
+  } else {
     issue_products<DIM>(p, smem, bars, walk, ctl);
   }
   __syncwarp();
