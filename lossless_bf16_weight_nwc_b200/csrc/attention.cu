@@ -10,8 +10,9 @@
 // rows of a prefix's whole group times the query heads of a key head; a
 // sequence's own tokens fill only a few of the 128, which costs nothing while
 // memory is the bound).  One persistent CTA an SM:
-//   * a producer warp brings K and V tiles of 128 tokens page by page with TMA
-//     into a ring;
+//   * a producer warp works out the CTA's parts, announces each to the others
+//     through a short queue in shared memory, and brings its K and V tiles of 128
+//     tokens page by page with TMA into a ring;
 //   * one thread issues S = Q K^T and O += P V (tcgen05, M = 128), with S, P and O
 //     in TMEM: P takes S's place as BF16 and is the A operand;
 //   * two teams of 128 softmax threads, a row each: a team holds its own 128 rows
@@ -40,8 +41,10 @@ constexpr int kProducerWarp = 8;
 constexpr int kIssuerWarp = 9;
 constexpr int kThreads = 10 * 32;
 constexpr int kMaxRing = 12;
+constexpr int kQueue = 5;                // parts announced ahead
 constexpr uint32_t kRingBytes = 163840;  // K and V tiles: 5 of dim 128, 10 of dim 64
-constexpr uint32_t kBarBytes = 1024;
+constexpr uint32_t kBarBytes = 3072;
+constexpr int kFewRows = 16;             // rows that the softmax warps multiply themselves
 constexpr float kLazy = 8.f;             // growth of the maximum (log2) that rescales O
 
 template <int DIM>
@@ -55,20 +58,46 @@ struct Layout {
 };
 static_assert(Layout<64>::kRing <= kMaxRing && Layout<128>::kBytes <= 232448, "shared memory");
 
+enum Kind : int32_t { kFew, kOne, kBoth };  // by rows: <= kFewRows, <= kTeamRows, more
+
+// A part as the producer announces it.
+struct Part {
+  int32_t n;       // tiles, 0: no more parts
+  int32_t kind;
+  int32_t far;     // of a prefix
+  int32_t seq0;    // first sequence of the segment
+  int32_t len;     // tokens of the segment
+  int32_t rows;    // of the block
+  int32_t base;    // first row of the block
+  int32_t kvh;     // key head
+  int32_t tile0;   // tiles [tile0, tile0 + n) of the segment
+  int64_t slot;    // of team 0's results, team 1's is the next; negative: none
+};
+struct Announced {
+  Part part;
+  int32_t limit[kFewRows];  // kFew: tokens of the segment that each row sees
+  int64_t q[kFewRows];      // and where its Q is (elements)
+};
+
 struct Bars {
   uint64_t full[kMaxRing];   // a tile's bytes landed
-  uint64_t empty[kMaxRing];  // the products that read the tile are done (2 arrivals)
+  uint64_t empty[kMaxRing];  // the tile has been read (8 arrivals, one a softmax warp)
+  uint64_t told[kQueue];     // a part is announced
+  uint64_t heard[kQueue];    // all have read it (9 arrivals: the softmax warps, the issuer)
   uint64_t qfull[2];         // the team's Q is in place
   uint64_t sfull[2];         // the team's S is in TMEM (and its P V before that is done)
   uint64_t pfull[2];         // the team's P is in TMEM (and V's tail is zeroed)
   uint64_t ofull[2];         // the last P V of the team's part is done
+  uint64_t team[2];          // the team's warps meet
   uint64_t drain;
   uint32_t tmem;
   uint32_t abort;
-  int32_t seg;               // where this CTA's share starts
-  int64_t off;
+  int32_t seg;               // the segment in which this CTA's share starts
+  int64_t start;             // and its place on the axis
   int64_t warp_flat[kThreads / 32];
   int32_t warp_items[kThreads / 32];
+  float2 ml[2][4][kFewRows]; // maximum and sum of each warp's rows in a part of few rows
+  Announced queue[kQueue];
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barriers");
 
@@ -80,8 +109,12 @@ struct Segment {
   int len;     // tokens
   int tiles;
   int items;
+  int shift;   // a tile costs 2^shift on the axis that is shared out
   bool far;    // a prefix
 };
+
+// What a tile costs by the rows of its segment (log2).
+constexpr int kCostFew = 1, kCostOne = 1, kCostBoth = 2;
 
 __device__ __forceinline__ int fresh_of(const BatchView& b, int seq) {
   return b.q_lens ? min(max(b.q_lens[seq], 0), b.chunk) : b.chunk;
@@ -112,69 +145,72 @@ __device__ __forceinline__ Segment segment(const AttentionParams& p, int s) {
   }
   r.tiles = (r.len + kKvTile - 1) / kKvTile;
   r.items = (r.rows + kPairRows - 1) / kPairRows * p.kv_heads;
+  r.shift = r.rows <= kFewRows ? kCostFew : r.rows <= kTeamRows ? kCostOne : kCostBoth;
   return r;
 }
-// CTAs that share `total` tiles out, and the first tile of CTA c.
-__device__ __forceinline__ int sharers(const AttentionParams& p, int64_t total) {
-  return (int)min((int64_t)p.ctas, max(total, (int64_t)1));
+// The tiles lie on an axis of costs; of `ctas` CTAs, c has those that start in
+// [share(c), share(c + 1)).  (Divisions of 64 bits are long: 32 where they do.)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
-__device__ __forceinline__ int64_t first_tile(int64_t total, int c, int ctas) {
-  return total * c / ctas;
+__device__ __forceinline__ int64_t share(int64_t total, int c, int ctas) {
+  return divide(total * c, ctas);
 }
-__device__ __forceinline__ int owner(int64_t total, int64_t tile, int ctas) {
-  return (int)(((tile + 1) * ctas - 1) / total);
+__device__ __forceinline__ int owner(int64_t total, int64_t at, int ctas) {
+  return (int)divide((at + 1) * ctas - 1, total);
 }
 
-struct Part {
-  Segment seg;
-  int s;           // segment
-  int block, kvh;  // block of kPairRows rows, key head
-  int rows;        // of the block
-  bool both;       // more than kTeamRows: each team has its own rows
-  int tile0, n;    // tiles [tile0, tile0 + n) of the segment
-  int item;        // within the segment
-};
+// The slot of a part's results for team 0: item + CTA is different for any two
+// parts, as each next part has a later item, a later CTA or both.
+__device__ __forceinline__ int64_t slot_of(const AttentionParams& p, int s, int item, int cta) {
+  const int64_t first =
+      s < p.batch.groups
+          ? reinterpret_cast<const int32_t*>(p.workspace + p.ws.items)[s]
+          : (int64_t)(s - p.batch.groups) * p.ws.own_items;
+  return (first + item + cta) * 2;
+}
 
-// The parts of a CTA in order.
+// The first tile at or behind `at` (>= 0) of a segment's axis.
+__device__ __forceinline__ int64_t tile_from(const Segment& g, int64_t at) {
+  return (at + (1 << g.shift) - 1) >> g.shift;
+}
+
+// The parts of a CTA in order: those of the tiles that start in [from, to) of the
+// axis, from segment s, which starts at `start`.
 struct Walk {
   int s;
-  int64_t off, left;
+  int64_t start, from, to;
   __device__ __forceinline__ bool next(const AttentionParams& p, Part& part) {
     const int segments = p.batch.groups + p.batch.sequences;
-    while (left > 0 && s < segments) {
-      part.seg = segment(p, s);
-      const int64_t flat = (int64_t)part.seg.tiles * part.seg.items;
-      if (off >= flat) {
+    while (s < segments && start < to) {
+      const Segment g = segment(p, s);
+      const int64_t all = (int64_t)g.tiles * g.items;
+      const int64_t t0 = from > start ? tile_from(g, from - start) : 0;
+      const int64_t t1 = min(all, tile_from(g, to - start));
+      if (t0 >= t1) {
+        start += all << g.shift;
         ++s;
-        off = 0;
         continue;
       }
-      part.s = s;
-      part.item = (int)(off / part.seg.tiles);
-      part.tile0 = (int)(off - (int64_t)part.item * part.seg.tiles);
-      part.n = (int)min((int64_t)(part.seg.tiles - part.tile0), left);
-      part.block = part.item / p.kv_heads;
-      part.kvh = part.item - part.block * p.kv_heads;
-      part.rows = min(part.seg.rows - part.block * kPairRows, kPairRows);
-      part.both = part.rows > kTeamRows;
-      off += part.n;
-      left -= part.n;
+      const int item = (int)divide(t0, g.tiles);
+      part.tile0 = (int)(t0 - (int64_t)item * g.tiles);
+      part.n = (int)min((int64_t)(g.tiles - part.tile0), t1 - t0);
+      const int block = item / p.kv_heads;
+      part.kvh = item - block * p.kv_heads;
+      part.base = block * kPairRows;
+      part.rows = min(g.rows - part.base, kPairRows);
+      part.kind = part.rows <= kFewRows ? kFew : part.rows <= kTeamRows ? kOne : kBoth;
+      part.far = g.far;
+      part.seq0 = g.seq0;
+      part.len = g.len;
+      part.slot = slot_of(p, s, item, (int)blockIdx.x);
+      if (part.slot >= (g.far ? p.ws.far_slots : p.ws.own_slots)) part.slot = -1;
+      from = start + ((t0 + part.n) << g.shift);
       return true;
     }
     return false;
   }
 };
-
-// The slot of a part's results for a team: item + CTA is different for any two
-// parts, as each next part has a later item, a later CTA or both.
-__device__ __forceinline__ int64_t slot_of(const AttentionParams& p, int s, int item, int cta,
-                                           int team) {
-  const int64_t first =
-      s < p.batch.groups
-          ? reinterpret_cast<const int32_t*>(p.workspace + p.ws.items)[s]
-          : (int64_t)(s - p.batch.groups) * p.ws.own_items;
-  return (first + item + cta) * 2 + team;
-}
 
 // ---- waits -------------------------------------------------------------------
 
@@ -199,7 +235,29 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Ctl& 
 
 // ---- roles ---------------------------------------------------------------------
 
-// Brings tile after tile: K at place 2n of the ring's sequence, V at 2n + 1.
+// The row of a part's block: which sequence, token and query head, and how many
+// of the segment's tokens it sees (0: padding).
+struct Row {
+  int64_t q;   // where its Q is (elements)
+  int limit;
+};
+__device__ __forceinline__ Row row_of(const AttentionParams& p, const Part& part, int r) {
+  const BatchView& b = p.batch;
+  const int gq = p.heads / p.kv_heads, per = b.chunk * gq, at = part.base + r;
+  const int sl = at / per, rest = at - sl * per, i = rest / gq;
+  const int seq = part.seq0 + sl, fresh = fresh_of(b, seq);
+  Row row;
+  row.q = (int64_t)(seq * b.chunk + i) * p.q.token_stride +
+          (int64_t)(part.kvh * gq + rest - i * gq) * p.q.head_stride;
+  row.limit = 0;
+  if (i < fresh)
+    row.limit =
+        part.far ? part.len : min(max(max(b.lens[seq], 0) - fresh + i + 1, 0), part.len);
+  return row;
+}
+
+// Announces part after part and brings its tiles: K at place 2n of the ring's
+// sequence, V at 2n + 1.
 template <int DIM>
 __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* k_map,
                            const CUtensorMap* v_map, uint8_t* smem, Bars* bars, Walk walk,
@@ -212,14 +270,33 @@ __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* k_map,
   const int mine = lane / kHalves, half = lane % kHalves;   // this lane's box and half of it
   const BatchView& b = p.batch;
   uint32_t seq = 0;
-  Part part;
   bool ok = true;
-  while (ok && walk.next(p, part)) {
-    const int32_t* row = part.seg.far ? b.prefix_table + (int64_t)part.s * b.prefix_stride
-                                      : b.table + (int64_t)part.seg.seq0 * b.table_stride;
+  for (uint32_t k = 0; ok; ++k) {
+    Part part;
+    part.n = 0;
+    part.kind = kOne;
+    const bool more = walk.next(p, part);
+    const uint32_t e = k % kQueue, turn = k / kQueue;
+    if (turn) ok = __all_sync(kAll, wait(&bars->heard[e], (turn - 1) & 1u, ctl));
+    if (!ok) break;
+    Announced& told = bars->queue[e];
+    if (more && part.kind == kFew && lane < part.rows) {
+      const Row row = row_of(p, part, lane);
+      told.limit[lane] = row.limit;
+      told.q[lane] = row.q;
+    }
+    if (lane == 0) told.part = part;
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&bars->told[e]);
+      if (more && part.slot < 0) atomicOr(p.cache.err, kErrRange);
+    }
+    if (!more) break;
+    const int32_t* row = part.far ? b.prefix_table + (int64_t)walk.s * b.prefix_stride
+                                  : b.table + (int64_t)part.seq0 * b.table_stride;
     for (int t = 0; t < part.n; ++t) {
       const int t0 = (part.tile0 + t) * kKvTile;
-      const int boxes = (min(kKvTile, part.seg.len - t0) + box - 1) / box;
+      const int boxes = (min(kKvTile, part.len - t0) + box - 1) / box;
       const bool on = mine < boxes;
       const int token = t0 + mine * box;
       int32_t id = 0;
@@ -230,10 +307,10 @@ __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* k_map,
           if (half == 0) atomicOr(p.cache.err, kErrRange);
         }
       }
-#pragma unroll
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++seq) {
-        const uint32_t slot = seq % L::kRing, turn = seq / L::kRing;
-        if (turn) ok = wait(&bars->empty[slot], (turn - 1) & 1u, ctl);
+        const uint32_t slot = seq % L::kRing, again = seq / L::kRing;
+        if (again) ok = wait(&bars->empty[slot], (again - 1) & 1u, ctl);
         ok = __all_sync(kAll, ok);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(&bars->full[slot], (uint32_t)(boxes * box * DIM * 2));
@@ -254,6 +331,19 @@ __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* k_map,
       wait_bounded(&bars->full[k % L::kRing], (k / L::kRing) & 1u, dc);
 }
 
+// Reads the next announced part (a whole warp); false when a wait gave up.  What
+// else the entry holds is read before `heard`.
+__device__ __forceinline__ bool hear(Bars* bars, uint32_t k, Part* part, const Ctl& ctl) {
+  const uint32_t e = k % kQueue;
+  if (!__all_sync(kAll, wait(&bars->told[e], (k / kQueue) & 1u, ctl))) return false;
+  *part = bars->queue[e].part;
+  return true;
+}
+__device__ __forceinline__ void heard(Bars* bars, uint32_t k) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->heard[k % kQueue]);
+}
+
 // One team's use of one tile, in the order the products are issued: teams in turn.
 struct Unit {
   uint32_t tile;   // of the CTA
@@ -261,25 +351,32 @@ struct Unit {
   bool last;       // the team's last of a part
 };
 struct Units {
-  Walk walk;
-  uint32_t tile = 0, team = 0;
+  uint32_t tile = 0, team = 0, k = 0;
   int left = 0, begun = 0;  // uses left of the part, teams that have begun it (bits)
-  bool both = false;
-  int next_n = 0;           // tiles of the part after it, 0: none
-  bool next_both = false;
-  __device__ __forceinline__ void look_ahead(const AttentionParams& p) {
-    Part part;
-    next_n = walk.next(p, part) ? part.n : 0;
-    next_both = part.both;
-  }
-  __device__ __forceinline__ bool next(const AttentionParams& p, Unit& u, uint32_t& team_out) {
-    if (left == 0) {
-      if (next_n == 0) return false;
-      both = next_both;
-      left = both ? 2 * next_n : next_n;
-      begun = 0;
-      look_ahead(p);
+  bool both = false, end = false;
+  // The next unit; false when there is none (end), or none yet while `pending` of
+  // the issuer's units still lack their P V: the softmax warps may need those to
+  // come to the part that follows, so the issuer must not wait for it.
+  __device__ __forceinline__ bool next(Bars* bars, const Ctl& ctl, int pending, Unit& u,
+                                       uint32_t& team_out) {
+    while (left == 0 && !end) {
+      const uint32_t e = k % kQueue;
+      if (pending > 0 && (!__all_sync(kAll, mbar_try_wait(&bars->told[e], (k / kQueue) & 1u)) ||
+                          bars->queue[e].part.kind == kFew))
+        return false;
+      Part part;
+      if (!hear(bars, k, &part, ctl)) part.n = 0;
+      heard(bars, k++);
+      end = part.n == 0;
+      if (part.kind == kFew) {   // the softmax warps multiply
+        tile += (uint32_t)part.n;
+      } else {
+        both = part.kind == kBoth;
+        left = both ? 2 * part.n : part.n;
+        begun = 0;
+      }
     }
+    if (end) return false;
     team_out = team;
     u.tile = tile;
     u.first = !(begun >> team & 1);
@@ -297,7 +394,7 @@ struct Units {
 // it follows a team's P V and the S of its next unit, and the team passes the
 // tiles it has then done with back to the producer.
 template <int DIM>
-__device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* bars, Walk walk,
+__device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* bars,
                                const Ctl& ctl) {
   using L = Layout<DIM>;
   const uint32_t leader = (threadIdx.x & 31) == 0;
@@ -307,8 +404,6 @@ __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* ba
   constexpr uint32_t id_o = umma_idesc_bf16_bmn(kTeamRows, DIM);
   uint32_t q_turn[2] = {0, 0}, p_turn[2] = {0, 0};
   Units units;
-  units.walk = walk;
-  units.look_ahead(p);
 
   auto issue_s = [&](const Unit& u, uint32_t w) -> bool {
     if (u.first && !wait(&bars->qfull[w], q_turn[w]++ & 1u, ctl)) return false;
@@ -339,15 +434,22 @@ __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* ba
     return true;
   };
 
-  Unit a, b, c;
-  uint32_t wa = 0, wb = 0, wc = 0;
-  bool has_a = units.next(p, a, wa) && issue_s(a, wa);
-  bool has_b = has_a && units.next(p, b, wb) && issue_s(b, wb);
-  while (has_a) {
-    if (!issue_o(a, wa)) break;
-    const bool has_c = has_b && units.next(p, c, wc) && issue_s(c, wc);
-    a = b, wa = wb, has_a = has_b;
-    b = c, wb = wc, has_b = has_c;
+  // S runs up to two units ahead of P V.
+  Unit unit[2], u;
+  uint32_t team[2], w;
+  int pending = 0;
+  for (;;) {
+    if (pending < 2 && units.next(bars, ctl, pending, u, w)) {
+      if (!issue_s(u, w)) break;
+      if (pending == 0) unit[0] = u, team[0] = w;
+      if (pending == 1) unit[1] = u, team[1] = w;
+      ++pending;
+      continue;
+    }
+    if (pending == 0) break;
+    if (!issue_o(unit[0], team[0])) break;
+    unit[0] = unit[1], team[0] = team[1];
+    --pending;
   }
   umma_commit_by(leader, &bars->drain);
   wait_bounded(&bars->drain, 0, drain_ctl_default(p.cache.err));
@@ -389,17 +491,217 @@ __device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo) + 0x8000u, __float_as_uint(hi) + 0x8000u, 0x7632);
 }
 
+// A part of at most kFewRows rows.  128 rows would keep the tensor cores busy with
+// padding for longer than memory takes to bring the tile, so each of the eight
+// softmax warps takes 16 tokens of every tile and multiplies them in registers
+// (m16n8k16: S^T = K Q^T with the tokens as M, O^T += V^T P^T with the elements as
+// M, G groups of eight rows as N), on its own until the part ends; then the
+// team's four warps join their maxima, sums and values through its Q buffer.
+template <int DIM, int G>
+__device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* smem, Bars* bars,
+                         const Ctl& ctl, uint32_t k, uint32_t tiles, uint32_t* meets, float c,
+                         uint32_t flip) {
+  using L = Layout<DIM>;
+  // Floats between rows in the buffer: four more spread the banks, where it fits.
+  constexpr int kStride = G == 1 ? DIM + 4 : DIM;
+  static_assert(4 * 8 * G * kStride * 4 <= L::kTile, "room to join the warps");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, q2 = 2 * (lane & 3);   // row and column pair of fragments
+  const uint32_t w = (uint32_t)warp >> 2;
+  // Fragments of Q^T: row g of each group; limits of rows q2 and q2 + 1.
+  const Announced& told = bars->queue[k % kQueue];
+  uint32_t qb[G][DIM / 16][2];
+  int limit[G][2];
+  const uint16_t* src[G];
+#pragma unroll
+  for (int n = 0; n < G; ++n) {
+    src[n] = 8 * n + g < part.rows ? static_cast<const uint16_t*>(p.q.data) + told.q[8 * n + g]
+                                   : nullptr;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      limit[n][j] = 8 * n + q2 + j < part.rows ? told.limit[8 * n + q2 + j] : 0;
+  }
+  heard(bars, k);
+#pragma unroll
+  for (int n = 0; n < G; ++n)
+#pragma unroll
+    for (int d = 0; d < DIM / 16; ++d)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        qb[n][d][j] =
+            src[n] ? *reinterpret_cast<const uint32_t*>(src[n] + 16 * d + 8 * j + q2) ^ flip : 0u;
+  float m[G][2], l[G][2], o[DIM / 16][G][4];
+#pragma unroll
+  for (int n = 0; n < G; ++n) {
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DIM / 16; ++d)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[d][n][j] = 0.f;
+  }
+  // Where this lane points ldmatrix.  K's four matrices: tokens 0-7, 8-15, then
+  // both with the next 8 elements; V's, transposed: elements 0-7, 8-15 of tokens
+  // 0-7, then both of tokens 8-15.
+  const int kt = 16 * warp + (lane & 15), kc = lane >> 4;
+  const int vt = 16 * warp + (lane & 7) + (lane >> 4) * 8, vc = (lane >> 3) & 1;
+  bool ok = true;
+  for (int t = 0; t < part.n; ++t) {
+    const int t0 = (part.tile0 + t) * kKvTile + 16 * warp;  // this warp's first token
+    const int there = part.len - t0;                        // of its tokens, how many are
+    const uint32_t ks = 2 * (tiles + (uint32_t)t), kslot = ks % L::kRing;
+    const uint32_t vs = ks + 1, vslot = vs % L::kRing;
+    ok = __all_sync(kAll, wait(&bars->full[kslot], (ks / L::kRing) & 1u, ctl));
+    if (!ok) break;
+    uint32_t pb[G][2];
+    if (there > 0) {
+      const uint32_t kb = smem_u32(smem + L::kRingOff + kslot * L::kTile) + (uint32_t)kt * 128u;
+      float s[G][2][4];
+#pragma unroll
+      for (int n = 0; n < G; ++n)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[n][j >> 2][j & 3] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DIM / 16; ++d) {
+        uint32_t a[4];
+        ldmatrix_x4(kb + (uint32_t)(d / 4) * (kKvTile * 128u) +
+                        (uint32_t)(((2 * d + kc) & 7) ^ (kt & 7)) * 16u,
+                    a);
+#pragma unroll
+        for (int n = 0; n < G; ++n)
+          mma_bf16_16816(s[n][d & 1], a[0], a[1], a[2], a[3], qb[n][d][0], qb[n][d][1]);
+      }
+#pragma unroll
+      for (int n = 0; n < G; ++n) {
+        float x[4], now[2];   // tokens g (rows q2, q2 + 1), then g + 8
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[j] = g + 8 * (j >> 1) < limit[n][j & 1] - t0 ? s[n][0][j] + s[n][1][j] : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          now[j] = fmaxf(x[j], x[j + 2]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) now[j] = fmaxf(now[j], __shfl_xor_sync(kAll, now[j], d));
+          now[j] = fmaxf(now[j], m[n][j]);
+        }
+        const bool grow0 = now[0] > m[n][0] && !((now[0] - m[n][0]) * c <= kLazy);
+        const bool grow1 = now[1] > m[n][1] && !((now[1] - m[n][1]) * c <= kLazy);
+        if (__any_sync(kAll, grow0 || grow1)) {
+          const float f0 =
+              !grow0 ? 1.f : m[n][0] == -INFINITY ? 0.f : exp2_approx((m[n][0] - now[0]) * c);
+          const float f1 =
+              !grow1 ? 1.f : m[n][1] == -INFINITY ? 0.f : exp2_approx((m[n][1] - now[1]) * c);
+#pragma unroll
+          for (int d = 0; d < DIM / 16; ++d) {
+            o[d][n][0] *= f0, o[d][n][2] *= f0;
+            o[d][n][1] *= f1, o[d][n][3] *= f1;
+          }
+          l[n][0] *= f0, l[n][1] *= f1;
+          if (grow0) m[n][0] = now[0];
+          if (grow1) m[n][1] = now[1];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float shift = m[n][j & 1] == -INFINITY ? 0.f : m[n][j & 1] * c;
+          x[j] = exp2_approx(fmaf(x[j], c, -shift));
+          l[n][j & 1] += x[j];
+        }
+        pb[n][0] = transpose_8x8(round_bf16x2(x[0], x[1]));
+        pb[n][1] = transpose_8x8(round_bf16x2(x[2], x[3]));
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->empty[kslot]);
+    ok = __all_sync(kAll, wait(&bars->full[vslot], (vs / L::kRing) & 1u, ctl));
+    if (!ok) break;
+    if (there > 0) {
+      // Tokens behind the segment's last count as zeros, whatever the page holds.
+      const int left = there - q2;
+      const uint32_t keep0 = (left > 0 ? 0xFFFFu : 0u) | (left > 1 ? 0xFFFF0000u : 0u);
+      const uint32_t keep1 = (left > 8 ? 0xFFFFu : 0u) | (left > 9 ? 0xFFFF0000u : 0u);
+      const uint32_t vb = smem_u32(smem + L::kRingOff + vslot * L::kTile) + (uint32_t)vt * 128u;
+#pragma unroll
+      for (int d = 0; d < DIM / 16; ++d) {
+        uint32_t a[4];
+        ldmatrix_x4_trans(vb + (uint32_t)(d / 4) * (kKvTile * 128u) +
+                              (uint32_t)(((2 * d + vc) & 7) ^ (vt & 7)) * 16u,
+                          a);
+        a[0] &= keep0, a[1] &= keep0, a[2] &= keep1, a[3] &= keep1;
+#pragma unroll
+        for (int n = 0; n < G; ++n)
+          mma_bf16_16816(o[d][n], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->empty[vslot]);
+  }
+  if (!ok) return false;
+  // Join the team's warps: values in its Q buffer.
+  const int tw = warp & 3;
+  float* buf = reinterpret_cast<float*>(smem + L::kQOff + w * L::kTile);
+#pragma unroll
+  for (int n = 0; n < G; ++n)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = 8 * n + q2 + j;
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[n][j] += __shfl_xor_sync(kAll, l[n][j], d);
+      if (row < part.rows) {
+        if (g == 0) bars->ml[w][tw][row] = make_float2(m[n][j] * c, l[n][j]);
+        float* dst = buf + (tw * 8 * G + row) * kStride + g;
+#pragma unroll
+        for (int d = 0; d < DIM / 16; ++d) {
+          dst[16 * d] = o[d][n][j];
+          dst[16 * d + 8] = o[d][n][j + 2];
+        }
+      }
+    }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bars->team[w]);
+  if (!__all_sync(kAll, wait(&bars->team[w], (*meets)++ & 1u, ctl))) return false;
+  const int slot_rows = part.far ? kTeamRows : p.ws.own_rows;
+  for (int row = tw; part.slot >= 0 && row < part.rows; row += 4) {
+    float top = -INFINITY, sum = 0.f, f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = fmaxf(top, bars->ml[w][j][row].x);
+    const float zero = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = exp2_approx(bars->ml[w][j][row].x - zero);
+      sum += f[j] * bars->ml[w][j][row].y;
+    }
+    const int64_t place = (part.slot + w) * slot_rows + row;
+    if (lane == 0)
+      reinterpret_cast<float2*>(p.workspace + (part.far ? p.ws.far_ml : p.ws.own_ml))[place] =
+          make_float2(top, sum);
+    float* dst =
+        reinterpret_cast<float*>(p.workspace + (part.far ? p.ws.far_o : p.ws.own_o)) + place * DIM;
+#pragma unroll
+    for (int d = 0; d < DIM; d += 64) {
+      float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = *reinterpret_cast<const float2*>(buf + (j * 8 * G + row) * kStride + d +
+                                                          2 * lane);
+        a.x += f[j] * x.x, a.y += f[j] * x.y;
+      }
+      *reinterpret_cast<float2*>(dst + d + 2 * lane) = a;
+    }
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bars->team[w]);
+  return __all_sync(kAll, wait(&bars->team[w], (*meets)++ & 1u, ctl));
+}
+
 // A softmax team: thread r has row r of the team's rows.
 template <int DIM>
-__device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars, Walk walk,
+__device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars,
                              const Ctl& ctl, uint32_t w) {
   using L = Layout<DIM>;
   const int r = threadIdx.x % kTeamThreads;
   const uint32_t lane_base = (uint32_t)(r & ~31) << 16;
   const uint32_t ts = bars->tmem + w * 128u + lane_base;         // S and P
   const uint32_t to = bars->tmem + 256u + w * 128u + lane_base;  // O
-  const BatchView& b = p.batch;
-  const int gq = p.heads / p.kv_heads;
   // Scores in units of log2; a negative scale turns Q's sign, which is exact, and
   // one of zero is replaced by one that leaves every finite score at zero (so that
   // masked scores of -inf stay what they are).
@@ -407,20 +709,30 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
   const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
   uint32_t turn = 0;       // this team's uses of tiles so far
   uint32_t done = 0;       // and its parts with at least one
+  uint32_t meets = 0;      // times the team's warps have met
   uint32_t uses = 0;       // both teams' uses so far
   uint32_t tiles = 0;      // tiles of the CTA so far
-  Part part;
-  bool more = walk.next(p, part);
-  while (more) {
-    // This thread's row: how many of the segment's tokens it sees.
-    const int base = part.block * kPairRows + (part.both ? (int)w * kTeamRows : 0);
-    const int team_rows = min(part.seg.rows - base, kTeamRows);
-    const int first = part.both ? 0 : (int)((uses ^ w) & 1u);    // the team's first tile
-    const int step = part.both ? 1 : 2;
+  for (uint32_t k = 0;; ++k) {
+    Part part;
+    if (!hear(bars, k, &part, ctl) || part.n == 0) return;
+    if (part.kind == kFew) {
+      const bool ok =
+          part.rows <= 8
+              ? few_part<DIM, 1>(p, part, smem, bars, ctl, k, tiles, &meets, c, flip)
+              : few_part<DIM, 2>(p, part, smem, bars, ctl, k, tiles, &meets, c, flip);
+      if (!ok) return;
+      tiles += (uint32_t)part.n;
+      continue;
+    }
+    heard(bars, k);
+    const bool both = part.kind == kBoth;
+    const int from = both ? (int)w * kTeamRows : 0;              // the team's first row
+    const int team_rows = min(part.rows - from, kTeamRows);
+    const int first = both ? 0 : (int)((uses ^ w) & 1u);         // the team's first tile
+    const int step = both ? 1 : 2;
     const int last = first + (part.n - 1 - first) / step * step;  // (when first < part.n)
-    const bool zeroes = !part.both || w == (uses & 1u);          // the tile's first user
+    const bool zeroes = !both || w == (uses & 1u);               // the tile's first user
     const bool begins = first < part.n;
-    const int per = b.chunk * gq;
     if (begins) {
       // Q's rows into the team's buffer: 16-byte pieces, 128-byte swizzle.  Rows
       // behind the last keep what is there: no row's result meets another's.
@@ -430,11 +742,8 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
                            (uint32_t)(piece / 8) * (kTeamRows * 128u);
 #pragma unroll 4
       for (int row = r / kPieces; row < team_rows; row += kStep) {
-        const int sl = (base + row) / per, rest = base + row - sl * per, i = rest / gq;
-        const uint4 v = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q.data) +
-            (int64_t)((part.seg.seq0 + sl) * b.chunk + i) * p.q.token_stride +
-            (int64_t)(part.kvh * gq + rest - i * gq) * p.q.head_stride)[piece];
+        const uint4 v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) +
+                                                       row_of(p, part, from + row).q)[piece];
         sts128(dst + (uint32_t)row * 128u + (uint32_t)((piece % 8) ^ (row & 7)) * 16u, v.x ^ flip,
                v.y ^ flip, v.z ^ flip, v.w ^ flip);
       }
@@ -442,16 +751,7 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
       tc_fence_before();
       mbar_arrive(&bars->qfull[w]);
     }
-    int limit = 0;
-    if (r < team_rows) {
-      const int sl = (base + r) / per, i = (base + r - sl * per) / gq;
-      const int seq = part.seg.seq0 + sl, fresh = fresh_of(b, seq);
-      if (i < fresh)
-        limit = part.seg.far ? part.seg.len
-                             : min(max(max(b.lens[seq], 0) - fresh + i + 1, 0), part.seg.len);
-    }
-    Part next;
-    more = walk.next(p, next);   // while the first scores are on their way
+    const int limit = r < team_rows ? row_of(p, part, from + r).limit : 0;
     float m = -INFINITY, l = 0.f;
     const bool warp_live = __any_sync(kAll, limit > 0);
     for (int t = first; t < part.n; t += step, ++turn) {
@@ -459,10 +759,10 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
       if (!__all_sync(kAll, wait(&bars->sfull[w], turn & 1u, ctl))) return;
       tc_fence_after();
       if (r == 0) {   // S is there: K has been read, and the V of the unit before
-        mbar_arrive_n(&bars->empty[2 * (tiles + (uint32_t)t) % L::kRing], part.both ? 1 : 2);
+        mbar_arrive_n(&bars->empty[2 * (tiles + (uint32_t)t) % L::kRing], both ? 4 : 8);
         if (t != first)
           mbar_arrive_n(&bars->empty[(2 * (tiles + (uint32_t)(t - step)) + 1) % L::kRing],
-                        part.both ? 1 : 2);
+                        both ? 4 : 8);
       }
       if (warp_live) {
         // Rows that are not there need no mask: nothing of theirs is read.
@@ -545,7 +845,7 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
         tmem_wait_store();
       }
       // Tokens behind the segment's last: whatever the pages hold there, V is zero.
-      const int there = part.seg.len - t0;
+      const int there = part.len - t0;
       if (there < kKvTile && zeroes) {
         const uint32_t seq = 2 * (tiles + (uint32_t)t) + 1, slot = seq % L::kRing;
         if (!__all_sync(kAll, wait(&bars->full[slot], (seq / L::kRing) & 1u, ctl))) return;
@@ -561,22 +861,20 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
       mbar_arrive(&bars->pfull[w]);
     }
     // The part's results.
-    const int64_t slot = slot_of(p, part.s, part.item, (int)blockIdx.x, (int)w);
-    const int slot_rows = part.seg.far ? kTeamRows : p.ws.own_rows;
-    const bool room = slot < (part.seg.far ? p.ws.far_slots : p.ws.own_slots);
-    const bool writes = r < team_rows && room;
-    float* o_at = reinterpret_cast<float*>(p.workspace +
-                                           (part.seg.far ? p.ws.far_o : p.ws.own_o)) +
-                  (slot * slot_rows + r) * DIM;
+    const int64_t place =
+        (part.slot + w) * (part.far ? kTeamRows : p.ws.own_rows) + r;
+    const bool writes = r < team_rows && part.slot >= 0;
+    float* o_at = reinterpret_cast<float*>(p.workspace + (part.far ? p.ws.far_o : p.ws.own_o)) +
+                  place * DIM;
     if (writes)
-      reinterpret_cast<float2*>(p.workspace + (part.seg.far ? p.ws.far_ml : p.ws.own_ml))
-          [slot * slot_rows + r] = make_float2(m * c, l);
+      reinterpret_cast<float2*>(p.workspace + (part.far ? p.ws.far_ml : p.ws.own_ml))[place] =
+          make_float2(m * c, l);
     if (begins) {
       if (!__all_sync(kAll, wait(&bars->ofull[w], done++ & 1u, ctl))) return;
       tc_fence_after();
       if (r == 0)
         mbar_arrive_n(&bars->empty[(2 * (tiles + (uint32_t)last) + 1) % L::kRing],
-                      part.both ? 1 : 2);
+                      both ? 4 : 8);
       if (warp_live) {
 #pragma unroll 1
         for (int k = 0; k < DIM; k += 32) {
@@ -594,10 +892,8 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
       }
       tc_fence_before();
     }
-    if (!room && r == 0) atomicOr(p.cache.err, kErrRange);
-    uses += (uint32_t)(part.both ? 2 * part.n : part.n);
+    uses += (uint32_t)(both ? 2 * part.n : part.n);
     tiles += (uint32_t)part.n;
-    part = next;
   }
 }
 
@@ -616,7 +912,7 @@ __device__ Walk share_out(const AttentionParams& p, Bars* bars) {
     flat = 0;
     if (s < segments) {
       const Segment g = segment(p, s);
-      flat = (int64_t)g.tiles * g.items;
+      flat = (int64_t)g.tiles * g.items << g.shift;
       n = g.items;
     }
     int64_t f = flat;
@@ -664,15 +960,15 @@ __device__ Walk share_out(const AttentionParams& p, Bars* bars) {
   }
   const int64_t total = run;
   if (blockIdx.x == 0 && threadIdx.x == 0) starts[segments] = total;
-  const int ctas = sharers(p, total);
   Walk walk;
   walk.s = 0;
-  walk.off = walk.left = 0;
-  if ((int)blockIdx.x >= ctas || total == 0) return walk;
-  const int64_t f0 = first_tile(total, (int)blockIdx.x, ctas);
-  const int64_t f1 = first_tile(total, (int)blockIdx.x + 1, ctas);
+  walk.start = walk.from = walk.to = 0;
+  if (total == 0) return walk;
+  const int64_t f0 = share(total, (int)blockIdx.x, p.ctas);
+  const int64_t f1 = share(total, (int)blockIdx.x + 1, p.ctas);
+  if (f0 == f1) return walk;
   if (segments <= kThreads) {
-    if (mine <= f0 && f0 < mine + mine_flat) bars->seg = (int)threadIdx.x, bars->off = f0 - mine;
+    if (mine <= f0 && f0 < mine + mine_flat) bars->seg = (int)threadIdx.x, bars->start = mine;
   } else {
     run = 0;
     run_items = 0;
@@ -680,13 +976,14 @@ __device__ Walk share_out(const AttentionParams& p, Bars* bars) {
       int32_t unused;
       scan(base, mine, mine_flat, unused);
       if (mine <= f0 && f0 < mine + mine_flat)
-        bars->seg = base + (int)threadIdx.x, bars->off = f0 - mine;
+        bars->seg = base + (int)threadIdx.x, bars->start = mine;
     }
   }
   __syncthreads();
   walk.s = bars->seg;
-  walk.off = bars->off;
-  walk.left = f1 - f0;
+  walk.start = bars->start;
+  walk.from = f0;
+  walk.to = f1;
   return walk;
 }
 
@@ -708,13 +1005,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int k = 0; k < L::kRing; ++k) {
       mbar_init(&bars->full[k], 1);
-      mbar_init(&bars->empty[k], 2);
+      mbar_init(&bars->empty[k], 8);
+    }
+    for (int k = 0; k < kQueue; ++k) {
+      mbar_init(&bars->told[k], 1);
+      mbar_init(&bars->heard[k], 9);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bars->qfull[w], kTeamThreads);
       mbar_init(&bars->sfull[w], 1);
       mbar_init(&bars->pfull[w], kTeamThreads);
       mbar_init(&bars->ofull[w], 1);
+      mbar_init(&bars->team[w], 4);
     }
     mbar_init(&bars->drain, 1);
     bars->abort = 0u;
@@ -732,11 +1034,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Walk walk = share_out(p, bars);
   const Ctl ctl{p.cache.err, p.wait_limit ? p.wait_limit : kDefaultWaitLimit, &bars->abort};
   if (warp < 8) {
-    softmax_team<DIM>(p, smem, bars, walk, ctl, (uint32_t)(warp >> 2));
+    softmax_team<DIM>(p, smem, bars, ctl, (uint32_t)(warp >> 2));
   } else if (warp == kProducerWarp) {
     produce_kv<DIM>(p, &k_map, &v_map, smem, bars, walk, ctl);
   } else {
-    issue_products<DIM>(p, smem, bars, walk, ctl);
+    issue_products<DIM>(p, smem, bars, ctl);
   }
   __syncwarp();
   tc_fence_before();
@@ -768,7 +1070,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int64_t* starts = reinterpret_cast<const int64_t*>(p.workspace + p.ws.starts);
   const int segments = b.groups + b.sequences;
   const int64_t total = starts[segments];
-  const int ctas = sharers(p, total);
   int group = -1;
   for (int g0 = 0; g0 < b.groups; g0 += 32) {
     const int g = g0 + lane;
@@ -792,8 +1093,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const int block = row / kPairRows, in_block = row - block * kPairRows;
     const bool both = min(seg.rows - block * kPairRows, kPairRows) > kTeamRows;
     const int item = block * p.kv_heads + kvh;
-    const int64_t t0 = starts[s] + (int64_t)item * seg.tiles;
-    const int c0 = owner(total, t0, ctas), c1 = owner(total, t0 + seg.tiles - 1, ctas);
+    const int64_t t0 = starts[s] + ((int64_t)item * seg.tiles << seg.shift);
+    const int c0 = owner(total, t0, p.ctas);
+    const int c1 = owner(total, t0 + ((int64_t)(seg.tiles - 1) << seg.shift), p.ctas);
     const int teams = both ? 1 : 2, team0 = both ? in_block / kTeamRows : 0;
     const int slot_rows = seg.far ? kTeamRows : p.ws.own_rows;
     const int64_t slots = seg.far ? p.ws.far_slots : p.ws.own_slots;
@@ -808,10 +1110,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       float2 v = make_float2(-INFINITY, 0.f);
       int64_t place = 0;
       if (k < parts) {
+        const int cta = c0 + k / teams;
         const int64_t slot =
-            slot_of(p, s, item, c0 + k / teams, both ? team0 : k - k / teams * teams);
+            slot_of(p, s, item, cta) + (both ? team0 : k - k / teams * teams);
+        // Where tiles cost more than a share, a CTA between may have none.
+        const int64_t from = share(total, cta, p.ctas);
+        const int64_t tile = from > t0 ? t0 + (tile_from(seg, from - t0) << seg.shift) : t0;
         place = slot * slot_rows + at;
-        if (slot < slots) v = ml[place];
+        if (slot < slots && tile < share(total, cta + 1, p.ctas)) v = ml[place];
       }
       float t = v.x;
 #pragma unroll

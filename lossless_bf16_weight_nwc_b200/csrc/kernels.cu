@@ -64,21 +64,6 @@ __device__ __forceinline__ WaitCtl drain_ctl(const TileParams& p) {
   return WaitCtl{p.err, p.wait_limit > kDefaultWaitLimit ? p.wait_limit : kDefaultWaitLimit};
 }
 
-// D += A B on the tensor cores, one warp: A is 16 x 16 BF16 (row-major
-// fragment a0..a3), B is 16 x 8 BF16 (column-major fragment b0, b1), D is
-// 16 x 8 FP32 (d0..d3).  Fragment of lane L (g = L / 4, c = L % 4):
-//   a0 = A[g][2c, 2c+1]   a1 = A[g+8][2c, 2c+1]   a2 = A[g][2c+8, 2c+9]   a3 = A[g+8][2c+8, 2c+9]
-//   b0 = B[2c, 2c+1][g]   b1 = B[2c+8, 2c+9][g]
-//   d0 = D[g][2c]   d1 = D[g][2c+1]   d2 = D[g+8][2c]   d3 = D[g+8][2c+1]
-// (the lower 16 bits of a register hold the first of its two elements).
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                               uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // ---- bit reader --------------------------------------------------------------
 
 // Per-lane reader of the lane's stream in shared memory, used with the 12-bit

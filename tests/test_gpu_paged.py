@@ -296,6 +296,16 @@ ATTEND = [  # lens, chunk, q_lens, heads, kw
     ([100, 20], 1, None, 128, dict(kv_heads=1, dim=128)),
     ([300], 3, None, 256, dict(kv_heads=2, dim=64)),
     ([20000], 64, None, 8, dict(kv_heads=2, dim=128, page=64)),
+    # Long and short shares of every kind of rows in turn, many parts an SM.
+    ([7 * i % 500 + 1 for i in range(64)], 1, None, 32,
+     dict(kv_heads=8, dim=128, prefix=[8200], starts=[0, 64])),
+    ([11 * i % 900 for i in range(90)], 1, None, 16,
+     dict(kv_heads=4, prefix=[3000, 5000, 700, 2600, 4000, 900], starts=[0, 2, 70, 74, 85, 86, 90])),
+    ([11 * i % 900 for i in range(90)], 1, None, 16,
+     dict(kv_heads=4, dim=128, prefix=[3000, 5000, 700, 2600, 4000, 900],
+          starts=[0, 2, 70, 74, 85, 86, 90])),
+    ([257] * 140, 3, None, 16, dict(kv_heads=4, dim=128, prefix=[1500] * 4,
+                                    starts=[0, 30, 35, 36, 140])),
 ]
 
 
