@@ -44,7 +44,6 @@ constexpr int kMaxRing = 12;
 constexpr int kQueue = 5;                // parts announced ahead
 constexpr uint32_t kRingBytes = 163840;  // K and V tiles: 5 of dim 128, 10 of dim 64
 constexpr uint32_t kBarBytes = 3072;
-constexpr int kFewRows = 16;             // rows that the softmax warps multiply themselves
 constexpr float kLazy = 8.f;             // growth of the maximum (log2) that rescales O
 
 template <int DIM>
@@ -58,7 +57,7 @@ struct Layout {
 };
 static_assert(Layout<64>::kRing <= kMaxRing && Layout<128>::kBytes <= 232448, "shared memory");
 
-enum Kind : int32_t { kFew, kOne, kBoth };  // by rows: <= kFewRows, <= kTeamRows, more
+enum Kind : int32_t { kFew, kOne, kBoth };  // rows: the segment <= kFewRows; <= kTeamRows; more
 
 // A part as the producer announces it.
 struct Part {
@@ -69,9 +68,9 @@ struct Part {
   int32_t len;     // tokens of the segment
   int32_t rows;    // of the block
   int32_t base;    // first row of the block
-  int32_t kvh;     // key head
+  int32_t kvh;     // key head, or the first of kFew's
   int32_t tile0;   // tiles [tile0, tile0 + n) of the segment
-  int64_t slot;    // of team 0's results, team 1's is the next; negative: none
+  int64_t place;   // first row of its results; negative: none
 };
 struct Announced {
   Part part;
@@ -101,6 +100,8 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barriers");
 
+constexpr int64_t kMaxTokens = 1ll << 30;  // of a segment: indexes stay in 31 bits
+
 // ---- segments, items and parts ---------------------------------------------
 
 struct Segment {
@@ -109,22 +110,26 @@ struct Segment {
   int len;     // tokens
   int tiles;
   int items;
-  int shift;   // a tile costs 2^shift on the axis that is shared out
+  bool few;    // at most kFewRows rows
+  int cost;    // of a tile on the axis that is shared out
+  int lead;    // of an item's start
   bool far;    // a prefix
 };
 
-// What a tile costs by the rows of its segment (log2).
-constexpr int kCostFew = 1, kCostOne = 1, kCostBoth = 2;
+// What a tile costs by the rows of its segment, and what each item adds at its start
+// (a part's beginning and end), in about 1000 cycles.
+constexpr int kCostFew = 2, kCostOne = 3, kCostBoth = 5;
+constexpr int kLeadFew = 2, kLeadOne = 6, kLeadBoth = 10;
 
 __device__ __forceinline__ int fresh_of(const BatchView& b, int seq) {
   return b.q_lens ? min(max(b.q_lens[seq], 0), b.chunk) : b.chunk;
 }
 __device__ __forceinline__ int own_len(const AttentionParams& p, int seq) {
-  const int64_t cap = (int64_t)p.batch.table_width << p.cache.page_shift;
+  const int64_t cap = min((int64_t)p.batch.table_width << p.cache.page_shift, kMaxTokens);
   return (int)min((int64_t)max(p.batch.lens[seq], 0), cap);
 }
 __device__ __forceinline__ int far_len(const AttentionParams& p, int g) {
-  const int64_t cap = (int64_t)p.batch.prefix_width << p.cache.page_shift;
+  const int64_t cap = min((int64_t)p.batch.prefix_width << p.cache.page_shift, kMaxTokens);
   return (int)min((int64_t)max(p.batch.prefix_lens[g], 0), cap);
 }
 __device__ __forceinline__ Segment segment(const AttentionParams& p, int s) {
@@ -143,9 +148,14 @@ __device__ __forceinline__ Segment segment(const AttentionParams& p, int s) {
     r.rows = b.chunk * gq;
     r.len = fresh_of(b, r.seq0) ? own_len(p, r.seq0) : 0;
   }
-  r.tiles = (r.len + kKvTile - 1) / kKvTile;
-  r.items = (r.rows + kPairRows - 1) / kPairRows * p.kv_heads;
-  r.shift = r.rows <= kFewRows ? kCostFew : r.rows <= kTeamRows ? kCostOne : kCostBoth;
+  r.few = r.rows <= kFewRows;
+  // Not (len + tile - 1) / tile, which may pass 31 bits.
+  const int tile = r.few ? p.few_tokens : kKvTile;
+  r.tiles = r.len / tile + (r.len % tile != 0);
+  r.items = r.few ? p.kv_heads / p.few_heads * (r.rows > 0)
+                  : (r.rows + kPairRows - 1) / kPairRows * p.kv_heads;
+  r.cost = r.few ? kCostFew : r.rows <= kTeamRows ? kCostOne : kCostBoth;
+  r.lead = r.few ? kLeadFew : r.rows <= kTeamRows ? kLeadOne : kLeadBoth;
   return r;
 }
 // The tiles lie on an axis of costs; of `ctas` CTAs, c has those that start in
@@ -160,52 +170,61 @@ __device__ __forceinline__ int owner(int64_t total, int64_t at, int ctas) {
   return (int)divide((at + 1) * ctas - 1, total);
 }
 
-// The slot of a part's results for team 0: item + CTA is different for any two
-// parts, as each next part has a later item, a later CTA or both.
+// The slot of a part's results: item + CTA is different for any two parts, as
+// each next part has a later item, a later CTA or both.
 __device__ __forceinline__ int64_t slot_of(const AttentionParams& p, int s, int item, int cta) {
   const int64_t first =
       s < p.batch.groups
           ? reinterpret_cast<const int32_t*>(p.workspace + p.ws.items)[s]
           : (int64_t)(s - p.batch.groups) * p.ws.own_items;
-  return (first + item + cta) * 2;
+  return first + item + cta;
 }
 
-// The first tile at or behind `at` (>= 0) of a segment's axis.
+// A segment's items on the axis: each a lead, then its tiles.
+__device__ __forceinline__ int64_t item_span(const Segment& g) {
+  return g.tiles ? g.lead + (int64_t)g.tiles * g.cost : 0;
+}
+// The first tile of the segment (counted over its items) that starts at or behind
+// `at` (>= 0) of its part of the axis.
 __device__ __forceinline__ int64_t tile_from(const Segment& g, int64_t at) {
-  return (at + (1 << g.shift) - 1) >> g.shift;
+  const int64_t span = item_span(g), item = divide(at, span), in = at - item * span - g.lead;
+  return item * g.tiles + (in > 0 ? divide(in + g.cost - 1, g.cost) : 0);
 }
 
 // The parts of a CTA in order: those of the tiles that start in [from, to) of the
-// axis, from segment s, which starts at `start`.
+// axis, from segment s, which starts at `start`; `tile`, the first one left of it.
 struct Walk {
   int s;
-  int64_t start, from, to;
+  int64_t start, from, to, tile;
   __device__ __forceinline__ bool next(const AttentionParams& p, Part& part) {
     const int segments = p.batch.groups + p.batch.sequences;
     while (s < segments && start < to) {
       const Segment g = segment(p, s);
-      const int64_t all = (int64_t)g.tiles * g.items;
-      const int64_t t0 = from > start ? tile_from(g, from - start) : 0;
-      const int64_t t1 = min(all, tile_from(g, to - start));
-      if (t0 >= t1) {
-        start += all << g.shift;
+      const int64_t span = item_span(g) * g.items;
+      if (tile < 0 && span > 0) tile = from > start ? tile_from(g, from - start) : 0;
+      const int64_t end =
+          to - start >= span ? (int64_t)g.tiles * g.items : tile_from(g, to - start);
+      if (tile >= end || span == 0) {
+        start += span;
+        tile = -1;
         ++s;
         continue;
       }
-      const int item = (int)divide(t0, g.tiles);
-      part.tile0 = (int)(t0 - (int64_t)item * g.tiles);
-      part.n = (int)min((int64_t)(g.tiles - part.tile0), t1 - t0);
-      const int block = item / p.kv_heads;
-      part.kvh = item - block * p.kv_heads;
+      const int item = (int)divide(tile, g.tiles);
+      part.tile0 = (int)(tile - (int64_t)item * g.tiles);
+      part.n = (int)min((int64_t)(g.tiles - part.tile0), end - tile);
+      const int block = g.few ? 0 : item / p.kv_heads;
+      part.kvh = g.few ? item * p.few_heads : item - block * p.kv_heads;
       part.base = block * kPairRows;
       part.rows = min(g.rows - part.base, kPairRows);
-      part.kind = part.rows <= kFewRows ? kFew : part.rows <= kTeamRows ? kOne : kBoth;
+      part.kind = g.few ? kFew : part.rows <= kTeamRows ? kOne : kBoth;
       part.far = g.far;
       part.seq0 = g.seq0;
       part.len = g.len;
-      part.slot = slot_of(p, s, item, (int)blockIdx.x);
-      if (part.slot >= (g.far ? p.ws.far_slots : p.ws.own_slots)) part.slot = -1;
-      from = start + ((t0 + part.n) << g.shift);
+      const int64_t slot = slot_of(p, s, item, (int)blockIdx.x);
+      const bool room = slot < (g.far ? p.ws.far_slots : p.ws.own_slots);
+      part.place = room ? slot * (g.far ? kPairRows : p.ws.own_rows) : -1;
+      tile += part.n;
       return true;
     }
     return false;
@@ -259,14 +278,12 @@ __device__ __forceinline__ Row row_of(const AttentionParams& p, const Part& part
 // Announces part after part and brings its tiles: K at place 2n of the ring's
 // sequence, V at 2n + 1.
 template <int DIM>
-__device__ void produce_kv(const AttentionParams& p, const CUtensorMap* k_map,
-                           const CUtensorMap* v_map, uint8_t* smem, Bars* bars, Walk walk,
-                           const Ctl& ctl) {
+__device__ void produce_kv(const AttentionParams& p, const CUtensorMap* maps, uint8_t* smem,
+                           Bars* bars, Walk walk, const Ctl& ctl) {
   using L = Layout<DIM>;
   constexpr int kHalves = DIM / 64;
   const int lane = threadIdx.x & 31;
   const int page = 1 << p.cache.page_shift;
-  const int box = min(page, kKvTile);
   const int mine = lane / kHalves, half = lane % kHalves;   // this lane's box and half of it
   const BatchView& b = p.batch;
   uint32_t seq = 0;
@@ -289,14 +306,23 @@ __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* k_map,
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(&bars->told[e]);
-      if (more && part.slot < 0) atomicOr(p.cache.err, kErrRange);
+      if (more && part.place < 0) atomicOr(p.cache.err, kErrRange);
     }
     if (!more) break;
     const int32_t* row = part.far ? b.prefix_table + (int64_t)walk.s * b.prefix_stride
                                   : b.table + (int64_t)part.seq0 * b.table_stride;
+    // A tile: kKvTile tokens of one head, rows of 128 bytes by halves of the head;
+    // or few_tokens of few_heads, by boxes, halves, heads.
+    const bool few = part.kind == kFew;
+    const int tile = few ? p.few_tokens : kKvTile;
+    const int box = min(page, tile);
+    const uint32_t box_bytes = (uint32_t)(box * (few ? p.few_heads : 1)) * 128u;
+    const uint32_t dst = few ? (uint32_t)lane * box_bytes
+                             : (uint32_t)(half * kKvTile + mine * box) * 128u;
+    const CUtensorMap* map = maps + (few ? 2 : 0);
     for (int t = 0; t < part.n; ++t) {
-      const int t0 = (part.tile0 + t) * kKvTile;
-      const int boxes = (min(kKvTile, part.len - t0) + box - 1) / box;
+      const int t0 = (part.tile0 + t) * tile;
+      const int boxes = (min(tile, part.len - t0) + box - 1) / box;
       const bool on = mine < boxes;
       const int token = t0 + mine * box;
       int32_t id = 0;
@@ -313,13 +339,12 @@ __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* k_map,
         if (again) ok = wait(&bars->empty[slot], (again - 1) & 1u, ctl);
         ok = __all_sync(kAll, ok);
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(&bars->full[slot], (uint32_t)(boxes * box * DIM * 2));
+        if (lane == 0)
+          mbar_expect_tx(&bars->full[slot], (uint32_t)(boxes * kHalves) * box_bytes);
         __syncwarp();
         if (on)
-          tma_load_4d(smem_u32(smem + L::kRingOff + slot * L::kTile) +
-                          (uint32_t)(half * kKvTile + mine * box) * 128u,
-                      kv ? v_map : k_map, half * 64, token & (page - 1), part.kvh, id,
-                      &bars->full[slot]);
+          tma_load_4d(smem_u32(smem + L::kRingOff + slot * L::kTile) + dst, map + kv, half * 64,
+                      token & (page - 1), part.kvh, id, &bars->full[slot]);
       }
       if (!ok) break;
     }
@@ -361,7 +386,7 @@ struct Units {
                                        uint32_t& team_out) {
     while (left == 0 && !end) {
       const uint32_t e = k % kQueue;
-      if (pending > 0 && (!__all_sync(kAll, mbar_try_wait(&bars->told[e], (k / kQueue) & 1u)) ||
+      if (pending > 0 && (!__all_sync(kAll, mbar_test_wait(&bars->told[e], (k / kQueue) & 1u)) ||
                           bars->queue[e].part.kind == kFew))
         return false;
       Part part;
@@ -434,16 +459,22 @@ __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* ba
     return true;
   };
 
-  // S runs up to two units ahead of P V.
+  // S runs up to two units ahead of P V, but does not wait for a part's Q while
+  // there are P V to issue: the team that loads it may need those.
   Unit unit[2], u;
   uint32_t team[2], w;
   int pending = 0;
+  bool has = false;
   for (;;) {
-    if (pending < 2 && units.next(bars, ctl, pending, u, w)) {
+    if (!has && pending < 2) has = units.next(bars, ctl, pending, u, w);
+    if (has && pending < 2 &&
+        (pending == 0 || !u.first ||
+         __all_sync(kAll, mbar_test_wait(&bars->qfull[w], q_turn[w] & 1u)))) {
       if (!issue_s(u, w)) break;
       if (pending == 0) unit[0] = u, team[0] = w;
       if (pending == 1) unit[1] = u, team[1] = w;
       ++pending;
+      has = false;
       continue;
     }
     if (pending == 0) break;
@@ -491,12 +522,15 @@ __device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo) + 0x8000u, __float_as_uint(hi) + 0x8000u, 0x7632);
 }
 
-// A part of at most kFewRows rows.  128 rows would keep the tensor cores busy with
-// padding for longer than memory takes to bring the tile, so each of the eight
-// softmax warps takes 16 tokens of every tile and multiplies them in registers
-// (m16n8k16: S^T = K Q^T with the tokens as M, O^T += V^T P^T with the elements as
-// M, G groups of eight rows as N), on its own until the part ends; then the
-// team's four warps join their maxima, sums and values through its Q buffer.
+// A part of a segment of at most kFewRows rows.  128 rows would keep the tensor
+// cores busy with padding for longer than memory takes to bring the tile, so each
+// of the eight softmax warps takes one head's 16 tokens of every tile and
+// multiplies them in registers (m16n8k16: S^T = K Q^T with the tokens as M, O^T +=
+// V^T P^T with the elements as M, G groups of eight rows as N), on its own until
+// the part ends.  A tile holds up to eight heads, so that a warp has a head to
+// itself, a page comes in two copies and a short sequence is one part; where there
+// are fewer heads, a team's warps of one head join their maxima, sums and values
+// through its Q buffer.
 template <int DIM, int G>
 __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* smem, Bars* bars,
                          const Ctl& ctl, uint32_t k, uint32_t tiles, uint32_t* meets, float c,
@@ -508,6 +542,8 @@ __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* sm
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q2 = 2 * (lane & 3);   // row and column pair of fragments
   const uint32_t w = (uint32_t)warp >> 2;
+  const int sharing = 8 / p.few_heads;            // warps of a head
+  const int hd = warp / sharing, sub = warp - hd * sharing;
   // Fragments of Q^T: row g of each group; limits of rows q2 and q2 + 1.
   const Announced& told = bars->queue[k % kQueue];
   uint32_t qb[G][DIM / 16][2];
@@ -515,8 +551,10 @@ __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* sm
   const uint16_t* src[G];
 #pragma unroll
   for (int n = 0; n < G; ++n) {
-    src[n] = 8 * n + g < part.rows ? static_cast<const uint16_t*>(p.q.data) + told.q[8 * n + g]
-                                   : nullptr;
+    src[n] = 8 * n + g < part.rows
+                 ? static_cast<const uint16_t*>(p.q.data) + told.q[8 * n + g] +
+                       (int64_t)(hd * (p.heads / p.kv_heads)) * p.q.head_stride
+                 : nullptr;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       limit[n][j] = 8 * n + q2 + j < part.rows ? told.limit[8 * n + q2 + j] : 0;
@@ -543,19 +581,26 @@ __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* sm
   // Where this lane points ldmatrix.  K's four matrices: tokens 0-7, 8-15, then
   // both with the next 8 elements; V's, transposed: elements 0-7, 8-15 of tokens
   // 0-7, then both of tokens 8-15.
-  const int kt = 16 * warp + (lane & 15), kc = lane >> 4;
-  const int vt = 16 * warp + (lane & 7) + (lane >> 4) * 8, vc = (lane >> 3) & 1;
+  const int box = min(1 << p.cache.page_shift, p.few_tokens);
+  const uint32_t half = (uint32_t)(box * p.few_heads) * 128u;   // bytes from half to half
+  auto row_at = [&](int token) -> uint32_t {                    // of this warp's head
+    const int n = token / box;
+    return (uint32_t)n * (DIM / 64) * half + (uint32_t)(hd * box + token - n * box) * 128u;
+  };
+  const int kc = lane >> 4, vc = (lane >> 3) & 1, l7 = lane & 7;
+  const uint32_t k_at = row_at(16 * sub + (lane & 15));
+  const uint32_t v_at = row_at(16 * sub + l7 + (lane >> 4) * 8);
   bool ok = true;
   for (int t = 0; t < part.n; ++t) {
-    const int t0 = (part.tile0 + t) * kKvTile + 16 * warp;  // this warp's first token
-    const int there = part.len - t0;                        // of its tokens, how many are
+    const int t0 = (part.tile0 + t) * p.few_tokens + 16 * sub;  // this warp's first token
+    const int there = part.len - t0;                            // of its tokens, how many are
     const uint32_t ks = 2 * (tiles + (uint32_t)t), kslot = ks % L::kRing;
     const uint32_t vs = ks + 1, vslot = vs % L::kRing;
     ok = __all_sync(kAll, wait(&bars->full[kslot], (ks / L::kRing) & 1u, ctl));
     if (!ok) break;
     uint32_t pb[G][2];
     if (there > 0) {
-      const uint32_t kb = smem_u32(smem + L::kRingOff + kslot * L::kTile) + (uint32_t)kt * 128u;
+      const uint32_t kb = smem_u32(smem + L::kRingOff + kslot * L::kTile) + k_at;
       float s[G][2][4];
 #pragma unroll
       for (int n = 0; n < G; ++n)
@@ -564,9 +609,8 @@ __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* sm
 #pragma unroll
       for (int d = 0; d < DIM / 16; ++d) {
         uint32_t a[4];
-        ldmatrix_x4(kb + (uint32_t)(d / 4) * (kKvTile * 128u) +
-                        (uint32_t)(((2 * d + kc) & 7) ^ (kt & 7)) * 16u,
-                    a);
+        ldmatrix_x4(
+            kb + (uint32_t)(d / 4) * half + (uint32_t)(((2 * d + kc) & 7) ^ l7) * 16u, a);
 #pragma unroll
         for (int n = 0; n < G; ++n)
           mma_bf16_16816(s[n][d & 1], a[0], a[1], a[2], a[3], qb[n][d][0], qb[n][d][1]);
@@ -619,13 +663,12 @@ __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* sm
       const int left = there - q2;
       const uint32_t keep0 = (left > 0 ? 0xFFFFu : 0u) | (left > 1 ? 0xFFFF0000u : 0u);
       const uint32_t keep1 = (left > 8 ? 0xFFFFu : 0u) | (left > 9 ? 0xFFFF0000u : 0u);
-      const uint32_t vb = smem_u32(smem + L::kRingOff + vslot * L::kTile) + (uint32_t)vt * 128u;
+      const uint32_t vb = smem_u32(smem + L::kRingOff + vslot * L::kTile) + v_at;
 #pragma unroll
       for (int d = 0; d < DIM / 16; ++d) {
         uint32_t a[4];
-        ldmatrix_x4_trans(vb + (uint32_t)(d / 4) * (kKvTile * 128u) +
-                              (uint32_t)(((2 * d + vc) & 7) ^ (vt & 7)) * 16u,
-                          a);
+        ldmatrix_x4_trans(
+            vb + (uint32_t)(d / 4) * half + (uint32_t)(((2 * d + vc) & 7) ^ l7) * 16u, a);
         a[0] &= keep0, a[1] &= keep0, a[2] &= keep1, a[3] &= keep1;
 #pragma unroll
         for (int n = 0; n < G; ++n)
@@ -636,16 +679,42 @@ __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* sm
     if (lane == 0) mbar_arrive(&bars->empty[vslot]);
   }
   if (!ok) return false;
-  // Join the team's warps: values in its Q buffer.
-  const int tw = warp & 3;
+#pragma unroll
+  for (int n = 0; n < G; ++n)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[n][j] += __shfl_xor_sync(kAll, l[n][j], d);
+  float2* ml_at = reinterpret_cast<float2*>(p.workspace + (part.far ? p.ws.far_ml : p.ws.own_ml));
+  float* o_at = reinterpret_cast<float*>(p.workspace + (part.far ? p.ws.far_o : p.ws.own_o));
+  // Results by heads, rows; of a single head by teams, rows.
+  const int64_t place =
+      part.place + (p.few_heads == 1 ? (int)w : hd) * (part.far ? kFewRows : p.ws.seq_rows);
+  if (sharing == 1) {
+#pragma unroll
+    for (int n = 0; n < G; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = 8 * n + q2 + j;
+        if (row < part.rows && part.place >= 0) {
+          if (g == 0) ml_at[place + row] = make_float2(m[n][j] * c, l[n][j]);
+          float* dst = o_at + (place + row) * DIM + g;
+#pragma unroll
+          for (int d = 0; d < DIM / 16; ++d) {
+            dst[16 * d] = o[d][n][j];
+            dst[16 * d + 8] = o[d][n][j + 2];
+          }
+        }
+      }
+    return true;
+  }
+  const int tw = warp & 3, mates = min(sharing, 4), tw0 = tw / mates * mates;
   float* buf = reinterpret_cast<float*>(smem + L::kQOff + w * L::kTile);
 #pragma unroll
   for (int n = 0; n < G; ++n)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int row = 8 * n + q2 + j;
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l[n][j] += __shfl_xor_sync(kAll, l[n][j], d);
       if (row < part.rows) {
         if (g == 0) bars->ml[w][tw][row] = make_float2(m[n][j] * c, l[n][j]);
         float* dst = buf + (tw * 8 * G + row) * kStride + g;
@@ -659,34 +728,28 @@ __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* sm
   __syncwarp();
   if (lane == 0) mbar_arrive(&bars->team[w]);
   if (!__all_sync(kAll, wait(&bars->team[w], (*meets)++ & 1u, ctl))) return false;
-  const int slot_rows = part.far ? kTeamRows : p.ws.own_rows;
-  for (int row = tw; part.slot >= 0 && row < part.rows; row += 4) {
-    float top = -INFINITY, sum = 0.f, f[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) top = fmaxf(top, bars->ml[w][j][row].x);
+  for (int row = tw - tw0; part.place >= 0 && row < part.rows; row += mates) {
+    float top = -INFINITY, sum = 0.f;
+    for (int j = 0; j < mates; ++j) top = fmaxf(top, bars->ml[w][tw0 + j][row].x);
     const float zero = top == -INFINITY ? 0.f : top;
+    float2 a[DIM / 64];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[j] = exp2_approx(bars->ml[w][j][row].x - zero);
-      sum += f[j] * bars->ml[w][j][row].y;
-    }
-    const int64_t place = (part.slot + w) * slot_rows + row;
-    if (lane == 0)
-      reinterpret_cast<float2*>(p.workspace + (part.far ? p.ws.far_ml : p.ws.own_ml))[place] =
-          make_float2(top, sum);
-    float* dst =
-        reinterpret_cast<float*>(p.workspace + (part.far ? p.ws.far_o : p.ws.own_o)) + place * DIM;
+    for (int d = 0; d < DIM / 64; ++d) a[d] = make_float2(0.f, 0.f);
+    for (int j = 0; j < mates; ++j) {
+      const float2 ml = bars->ml[w][tw0 + j][row];
+      const float f = exp2_approx(ml.x - zero);
+      sum += f * ml.y;
 #pragma unroll
-    for (int d = 0; d < DIM; d += 64) {
-      float2 a = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = *reinterpret_cast<const float2*>(buf + (j * 8 * G + row) * kStride + d +
-                                                          2 * lane);
-        a.x += f[j] * x.x, a.y += f[j] * x.y;
+      for (int d = 0; d < DIM / 64; ++d) {
+        const float2 x = *reinterpret_cast<const float2*>(
+            buf + ((tw0 + j) * 8 * G + row) * kStride + 64 * d + 2 * lane);
+        a[d].x += f * x.x, a[d].y += f * x.y;
       }
-      *reinterpret_cast<float2*>(dst + d + 2 * lane) = a;
     }
+    if (lane == 0) ml_at[place + row] = make_float2(top, sum);
+#pragma unroll
+    for (int d = 0; d < DIM / 64; ++d)
+      *reinterpret_cast<float2*>(o_at + (place + row) * DIM + 64 * d + 2 * lane) = a[d];
   }
   __syncwarp();
   if (lane == 0) mbar_arrive(&bars->team[w]);
@@ -733,25 +796,35 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
     const int last = first + (part.n - 1 - first) / step * step;  // (when first < part.n)
     const bool zeroes = !both || w == (uses & 1u);               // the tile's first user
     const bool begins = first < part.n;
+    // This thread's row; a team without a tile only leaves word that it has nothing.
+    Row mine;
+    mine.q = mine.limit = 0;
+    if (begins && r < team_rows) mine = row_of(p, part, from + r);
+    const int limit = mine.limit;
     if (begins) {
-      // Q's rows into the team's buffer: 16-byte pieces, 128-byte swizzle.  Rows
-      // behind the last keep what is there: no row's result meets another's.
-      constexpr int kPieces = DIM / 8, kStep = kTeamThreads / kPieces;
-      const int piece = r % kPieces;
+      // Q's rows into the team's buffer: 16-byte pieces, 128-byte swizzle, each
+      // warp its own 32.  Rows behind the last get the tensor's first: no row's
+      // result meets another's.
+      constexpr int kPieces = DIM / 8, kStep = 32 / kPieces;
+      const int lane = r & 31, piece = lane % kPieces;
       const uint32_t dst = smem_u32(smem + L::kQOff + w * L::kTile) +
                            (uint32_t)(piece / 8) * (kTeamRows * 128u);
-#pragma unroll 4
-      for (int row = r / kPieces; row < team_rows; row += kStep) {
-        const uint4 v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) +
-                                                       row_of(p, part, from + row).q)[piece];
-        sts128(dst + (uint32_t)row * 128u + (uint32_t)((piece % 8) ^ (row & 7)) * 16u, v.x ^ flip,
-               v.y ^ flip, v.z ^ flip, v.w ^ flip);
+      uint4 v[kPieces];   // all loads before the first store, which the compiler keeps in order
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int64_t at = __shfl_sync(kAll, mine.q, j * kStep + lane / kPieces);
+        v[j] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) + at)[piece];
+      }
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int in = (r & ~31) + j * kStep + lane / kPieces;
+        sts128(dst + (uint32_t)in * 128u + (uint32_t)((piece % 8) ^ (in & 7)) * 16u, v[j].x ^ flip,
+               v[j].y ^ flip, v[j].z ^ flip, v[j].w ^ flip);
       }
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(&bars->qfull[w]);
     }
-    const int limit = r < team_rows ? row_of(p, part, from + r).limit : 0;
     float m = -INFINITY, l = 0.f;
     const bool warp_live = __any_sync(kAll, limit > 0);
     for (int t = first; t < part.n; t += step, ++turn) {
@@ -861,13 +934,11 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
       mbar_arrive(&bars->pfull[w]);
     }
     // The part's results.
-    const int64_t place =
-        (part.slot + w) * (part.far ? kTeamRows : p.ws.own_rows) + r;
-    const bool writes = r < team_rows && part.slot >= 0;
-    float* o_at = reinterpret_cast<float*>(p.workspace + (part.far ? p.ws.far_o : p.ws.own_o)) +
-                  place * DIM;
-    if (writes)
-      reinterpret_cast<float2*>(p.workspace + (part.far ? p.ws.far_ml : p.ws.own_ml))[place] =
+    const int64_t place = part.place + (int)w * (part.far ? kTeamRows : p.ws.own_rows / 2);
+    float* o_at = reinterpret_cast<float*>(p.workspace + (part.far ? p.ws.far_o : p.ws.own_o));
+    if (r < team_rows && part.place >= 0)
+      reinterpret_cast<float2*>(p.workspace +
+                                (part.far ? p.ws.far_ml : p.ws.own_ml))[place + r] =
           make_float2(m * c, l);
     if (begins) {
       if (!__all_sync(kAll, wait(&bars->ofull[w], done++ & 1u, ctl))) return;
@@ -876,21 +947,41 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
         mbar_arrive_n(&bars->empty[(2 * (tiles + (uint32_t)last) + 1) % L::kRing],
                       both ? 4 : 8);
       if (warp_live) {
+        // Rows of a lane each become rows of a warp through the Q buffer (pieces of
+        // 16 bytes, spread over the banks): a lane's own row of 512 bytes stored
+        // piece by piece touched 32 lines a store, 8,000 cycles a part.
+        constexpr int kCols = DIM / 2, kPieces = kCols / 4;
+        const int lane = r & 31, wrow = r & ~31;
+        const uint32_t buf = smem_u32(smem + L::kQOff + w * L::kTile) +
+                             (uint32_t)(r >> 5) * (L::kTile / 4);
 #pragma unroll 1
-        for (int k = 0; k < DIM; k += 32) {
-          float o[32];
-          tmem_load32(to + (uint32_t)k, o);
-          tmem_wait_load();
-          tmem_tie<32>(o);
-          if (writes) {
+        for (int k = 0; k < DIM; k += kCols) {
+          float o[kCols];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              reinterpret_cast<float4*>(o_at + k)[j] =
-                  make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          for (int j = 0; j < kCols; j += 32) tmem_load32(to + (uint32_t)(k + j), o + j);
+          tmem_wait_load();
+          tmem_tie<kCols>(o);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j)
+            sts128(buf + (uint32_t)(lane * kPieces + (j ^ (lane & 7))) * 16u,
+                   __float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]),
+                   __float_as_uint(o[4 * j + 2]), __float_as_uint(o[4 * j + 3]));
+          __syncwarp();
+          const int piece = lane % kPieces;
+#pragma unroll 8
+          for (int row = lane / kPieces; row < 32; row += 32 / kPieces) {
+            const uint4 v = lds128(buf + (uint32_t)(row * kPieces + (piece ^ (row & 7))) * 16u);
+            if (wrow + row < team_rows && part.place >= 0)
+              reinterpret_cast<uint4*>(o_at + (place + wrow + row) * DIM + k)[piece] = v;
           }
         }
       }
       tc_fence_before();
+      // The buffer is the whole team's again.
+      __syncwarp();
+      if ((r & 31) == 0) mbar_arrive(&bars->team[w]);
+      if (!__all_sync(kAll, wait(&bars->team[w], meets++ & 1u, ctl))) return;
     }
     uses += (uint32_t)(both ? 2 * part.n : part.n);
     tiles += (uint32_t)part.n;
@@ -898,26 +989,38 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
 }
 
 // First tile and first item of every segment, by a scan of the whole CTA; finds
-// this CTA's share.  CTA 0 writes them down for the kernel that joins the parts.
+// this CTA's share.  CTA 0 writes the starts down for the kernel that joins the
+// parts, and reports lengths that the tables do not hold.
 __device__ Walk share_out(const AttentionParams& p, Bars* bars) {
-  const int segments = p.batch.groups + p.batch.sequences;
+  const BatchView& b = p.batch;
+  const int segments = b.groups + b.sequences;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t* starts = reinterpret_cast<int64_t*>(p.workspace + p.ws.starts);
   int32_t* items = reinterpret_cast<int32_t*>(p.workspace + p.ws.items);
-  int64_t run = 0, mine = 0, mine_flat = 0;
+  const int chunks = (segments + kThreads - 1) / kThreads;
+  int64_t run = 0, f0 = -1, f1 = 0;
   int32_t run_items = 0;
-  auto scan = [&](int base, int64_t& before, int64_t& flat, int32_t& before_items) {
-    const int s = base + (int)threadIdx.x;
+  // Up to kThreads segments at a time for the total, then once more (unless there
+  // is but one time) to find the segment of the share's start.
+#pragma unroll 1
+  for (int turn = 0; turn < 2 * chunks - (chunks == 1); ++turn) {
+    if (turn == chunks) {
+      f0 = share(run, (int)blockIdx.x, p.ctas);
+      f1 = share(run, (int)blockIdx.x + 1, p.ctas);
+      run = 0;
+      run_items = 0;
+    }
+    const int s = (turn < chunks ? turn : turn - chunks) * kThreads + (int)threadIdx.x;
     int32_t n = 0;
-    flat = 0;
+    int64_t flat = 0;
     if (s < segments) {
       const Segment g = segment(p, s);
-      flat = (int64_t)g.tiles * g.items << g.shift;
+      flat = item_span(g) * g.items;
       n = g.items;
     }
     int64_t f = flat;
     int32_t m = n;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t f2 = __shfl_up_sync(kAll, f, o);
       const int32_t m2 = __shfl_up_sync(kAll, m, o);
@@ -926,60 +1029,38 @@ __device__ Walk share_out(const AttentionParams& p, Bars* bars) {
     __syncthreads();
     if (lane == 31) bars->warp_flat[warp] = f, bars->warp_items[warp] = m;
     __syncthreads();
-    int64_t all = 0, low = 0;
-    int32_t all_items = 0, low_items = 0;
+    int64_t before = run + f - flat;
+    int32_t before_items = run_items + m - n;
 #pragma unroll
     for (int k = 0; k < kThreads / 32; ++k) {
-      if (k == warp) low = all, low_items = all_items;
-      all += bars->warp_flat[k];
-      all_items += bars->warp_items[k];
+      if (k < warp) before += bars->warp_flat[k], before_items += bars->warp_items[k];
+      run += bars->warp_flat[k];
+      run_items += bars->warp_items[k];
     }
-    before = run + low + f - flat;
-    before_items = run_items + low_items + m - n;
-    run += all;
-    run_items += all_items;
-  };
-  for (int base = 0; base < segments; base += kThreads) {
-    int32_t mine_items;
-    scan(base, mine, mine_flat, mine_items);
-    const int s = base + (int)threadIdx.x;
+    if (chunks == 1) {
+      f0 = share(run, (int)blockIdx.x, p.ctas);
+      f1 = share(run, (int)blockIdx.x + 1, p.ctas);
+    }
     if (s < segments) {
       // Every CTA needs its prefixes' first items for its slots: all write the
       // same values.
-      if (s < p.batch.groups) items[s] = mine_items;
-      if (blockIdx.x == 0) {
-        starts[s] = mine;
-        const bool over = s < p.batch.groups
-                              ? p.batch.prefix_lens[s] > far_len(p, s) && p.batch.prefix_lens[s] > 0
-                              : p.batch.lens[s - p.batch.groups] > 0 &&
-                                    p.batch.lens[s - p.batch.groups] >
-                                        own_len(p, s - p.batch.groups);
-        if (over) atomicOr(p.cache.err, kErrRange);
+      if (s < b.groups) items[s] = before_items;
+      if (blockIdx.x == 0 && turn < chunks) {
+        starts[s] = before;
+        const int len = s < b.groups ? b.prefix_lens[s] : b.lens[s - b.groups];
+        if (len > (s < b.groups ? far_len(p, s) : own_len(p, s - b.groups)) && len > 0)
+          atomicOr(p.cache.err, kErrRange);
       }
+      if (before <= f0 && f0 < before + flat) bars->seg = s, bars->start = before;
     }
   }
-  const int64_t total = run;
-  if (blockIdx.x == 0 && threadIdx.x == 0) starts[segments] = total;
+  if (blockIdx.x == 0 && threadIdx.x == 0) starts[segments] = run;
+  __syncthreads();
   Walk walk;
   walk.s = 0;
   walk.start = walk.from = walk.to = 0;
-  if (total == 0) return walk;
-  const int64_t f0 = share(total, (int)blockIdx.x, p.ctas);
-  const int64_t f1 = share(total, (int)blockIdx.x + 1, p.ctas);
-  if (f0 == f1) return walk;
-  if (segments <= kThreads) {
-    if (mine <= f0 && f0 < mine + mine_flat) bars->seg = (int)threadIdx.x, bars->start = mine;
-  } else {
-    run = 0;
-    run_items = 0;
-    for (int base = 0; base < segments && run <= f0; base += kThreads) {
-      int32_t unused;
-      scan(base, mine, mine_flat, unused);
-      if (mine <= f0 && f0 < mine + mine_flat)
-        bars->seg = base + (int)threadIdx.x, bars->start = mine;
-    }
-  }
-  __syncthreads();
+  walk.tile = -1;
+  if (f0 >= f1) return walk;
   walk.s = bars->seg;
   walk.start = bars->start;
   walk.from = f0;
@@ -990,8 +1071,7 @@ __device__ Walk share_out(const AttentionParams& p, Bars* bars) {
 template <int DIM>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ AttentionParams p,
-                     const __grid_constant__ CUtensorMap k_map,
-                     const __grid_constant__ CUtensorMap v_map) {
+                     const __grid_constant__ PageMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem_attention[];
   uint8_t* smem = smem_attention;
   using L = Layout<DIM>;
@@ -1036,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 8) {
     softmax_team<DIM>(p, smem, bars, ctl, (uint32_t)(warp >> 2));
   } else if (warp == kProducerWarp) {
-    produce_kv<DIM>(p, &k_map, &v_map, smem, bars, walk, ctl);
+    produce_kv<DIM>(p, maps.map, smem, bars, walk, ctl);
   } else {
     issue_products<DIM>(p, smem, bars, ctl);
   }
@@ -1050,26 +1130,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---- joining the parts ------------------------------------------------------------
 
 constexpr int kJoinWarps = 4;
+constexpr int kJoinThreads = kJoinWarps * 32;
 
-// One warp a row and query head: over the parts of its prefix and its own tokens,
-// out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i, in order.
+// Where a row's results lie in a segment's parts.
+struct Side {
+  int64_t t0;      // where its item's first tile starts on the axis
+  int s, item, cost, c0;
+  int n, teams;    // results: CTAs from c0 on, times teams that have the row each
+  int at, team_rows, part_rows;
+  bool far;
+};
+
+// One CTA a row and query head: over the parts of its prefix and its own tokens,
+// out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i, in a fixed order.  A thread a
+// part for the weights, then a warp a part for the values, four parts in flight.
 template <int DIM>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+__global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const __grid_constant__ AttentionParams p) {
   constexpr int E = DIM / 32;
+  __shared__ float weight[kJoinThreads];
+  __shared__ const float* source[kJoinThreads];
+  __shared__ float values[kJoinWarps][DIM];
+  __shared__ float red[2][kJoinWarps];
   allow_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const BatchView& b = p.batch;
-  const int64_t rows = (int64_t)b.sequences * b.chunk;
-  if (id >= rows * p.heads) return;
-  const int token = (int)(id / p.heads), head = (int)(id - (int64_t)token * p.heads);
+  const int token = (int)(blockIdx.x / (unsigned)p.heads);
+  const int head = (int)(blockIdx.x - (unsigned)token * (unsigned)p.heads);
   const int seq = token / b.chunk, i = token - seq * b.chunk;
   const int gq = p.heads / p.kv_heads, kvh = head / gq, h = head - kvh * gq;
   wait_prerequisites();
   const int64_t* starts = reinterpret_cast<const int64_t*>(p.workspace + p.ws.starts);
-  const int segments = b.groups + b.sequences;
-  const int64_t total = starts[segments];
+  const int64_t total = starts[b.groups + b.sequences];
   int group = -1;
   for (int g0 = 0; g0 < b.groups; g0 += 32) {
     const int g = g0 + lane;
@@ -1080,88 +1172,132 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       break;
     }
   }
+  const bool real = i < fresh_of(b, seq);
+  auto side_of = [&](int s) {
+    Side d;
+    d.n = 0;
+    if (!real || s < 0) return d;
+    const Segment seg = segment(p, s);
+    if (seg.tiles == 0) return d;
+    const int row = ((seq - seg.seq0) * b.chunk + i) * gq + h;
+    const int block = row / kPairRows, in_block = row - block * kPairRows;
+    const bool both = !seg.few && min(seg.rows - block * kPairRows, kPairRows) > kTeamRows;
+    d.s = s;
+    d.far = seg.far;
+    d.cost = seg.cost;
+    d.item = seg.few ? kvh / p.few_heads : block * p.kv_heads + kvh;
+    d.t0 = starts[s] + item_span(seg) * d.item + seg.lead;
+    d.c0 = owner(total, d.t0, p.ctas);
+    // A part has the row once, or for each of the two teams that share it.
+    d.teams = seg.few ? (p.few_heads == 1 ? 2 : 1) : both ? 1 : 2;
+    d.n = (owner(total, d.t0 + (int64_t)(seg.tiles - 1) * seg.cost, p.ctas) - d.c0 + 1) *
+          d.teams;
+    d.team_rows = seg.few  ? (seg.far ? kFewRows : p.ws.seq_rows)
+                  : seg.far ? kTeamRows
+                            : p.ws.own_rows / 2;
+    d.at = seg.few ? (p.few_heads == 1 ? 0 : kvh % p.few_heads) * d.team_rows + row
+           : both  ? in_block / kTeamRows * d.team_rows + in_block % kTeamRows
+                   : in_block;
+    d.part_rows = seg.far ? kPairRows : p.ws.own_rows;
+    return d;
+  };
+  const Side far = side_of(group), own = side_of(b.groups + seq);
   float top = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  const bool real = i < fresh_of(b, seq);
-  for (int side = 0; real && side < 2; ++side) {
-    const int s = side == 0 ? group : b.groups + seq;
-    if (s < 0) continue;
-    const Segment seg = segment(p, s);
-    if (seg.tiles == 0) continue;
-    const int row = ((seq - seg.seq0) * b.chunk + i) * gq + h;
-    const int block = row / kPairRows, in_block = row - block * kPairRows;
-    const bool both = min(seg.rows - block * kPairRows, kPairRows) > kTeamRows;
-    const int item = block * p.kv_heads + kvh;
-    const int64_t t0 = starts[s] + ((int64_t)item * seg.tiles << seg.shift);
-    const int c0 = owner(total, t0, p.ctas);
-    const int c1 = owner(total, t0 + ((int64_t)(seg.tiles - 1) << seg.shift), p.ctas);
-    const int teams = both ? 1 : 2, team0 = both ? in_block / kTeamRows : 0;
-    const int slot_rows = seg.far ? kTeamRows : p.ws.own_rows;
-    const int64_t slots = seg.far ? p.ws.far_slots : p.ws.own_slots;
-    const float2* ml =
-        reinterpret_cast<const float2*>(p.workspace + (seg.far ? p.ws.far_ml : p.ws.own_ml));
-    const float* o =
-        reinterpret_cast<const float*>(p.workspace + (seg.far ? p.ws.far_o : p.ws.own_o));
-    const int at = both ? in_block - team0 * kTeamRows : in_block;
-    const int parts = (c1 - c0 + 1) * teams;
-    for (int k0 = 0; k0 < parts; k0 += 32) {
-      const int k = k0 + lane;
-      float2 v = make_float2(-INFINITY, 0.f);
-      int64_t place = 0;
-      if (k < parts) {
-        const int cta = c0 + k / teams;
-        const int64_t slot =
-            slot_of(p, s, item, cta) + (both ? team0 : k - k / teams * teams);
-        // Where tiles cost more than a share, a CTA between may have none.
-        const int64_t from = share(total, cta, p.ctas);
-        const int64_t tile = from > t0 ? t0 + (tile_from(seg, from - t0) << seg.shift) : t0;
-        place = slot * slot_rows + at;
-        if (slot < slots && tile < share(total, cta + 1, p.ctas)) v = ml[place];
-      }
-      float t = v.x;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, d));
-      const float now = fmaxf(top, t);
-      const float base = now == -INFINITY ? 0.f : now;
-      const float keep = exp2f(top - base);
-      sum *= keep;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= keep;
-      top = now;
-      // A part without weight is not read (its values were not written).
-      const float f = v.y != 0.f ? exp2f(v.x - base) : 0.f;
-      unsigned live = __ballot_sync(kAll, v.y != 0.f);
-      while (live) {
-        const int j = __ffs(live) - 1;
-        live &= live - 1;
-        const float fj = __shfl_sync(kAll, f, j);
-        sum += fj * __shfl_sync(kAll, v.y, j);
-        const int64_t pj = __shfl_sync(kAll, place, j);
-        const float* src = o + pj * DIM + lane * E;
-        if (E == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src);
-          acc[0] += fj * x.x, acc[1] += fj * x.y, acc[2 % E] += fj * x.z, acc[3 % E] += fj * x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(src);
-          acc[0] += fj * x.x, acc[1] += fj * x.y;
-        }
+  for (int k0 = 0; k0 < far.n + own.n; k0 += kJoinThreads) {
+    const int count = min(far.n + own.n - k0, kJoinThreads);
+    float2 v = make_float2(-INFINITY, 0.f);
+    const float* src = nullptr;
+    if ((int)threadIdx.x < count) {
+      const bool in_far = k0 + (int)threadIdx.x < far.n;
+      const Side& d = in_far ? far : own;
+      const int k = k0 + (int)threadIdx.x - (in_far ? 0 : far.n);
+      const int cta = d.c0 + k / d.teams;
+      // Where a tile costs more than a share, a CTA between may have none.
+      const int64_t from = share(total, cta, p.ctas);
+      const int64_t tile =
+          from > d.t0 ? d.t0 + divide(from - d.t0 + d.cost - 1, d.cost) * d.cost : d.t0;
+      const int64_t slot = slot_of(p, d.s, d.item, cta);
+      const int64_t place = slot * d.part_rows + k % d.teams * d.team_rows + d.at;
+      if (slot < (d.far ? p.ws.far_slots : p.ws.own_slots) &&
+          tile < share(total, cta + 1, p.ctas)) {
+        v = reinterpret_cast<const float2*>(p.workspace +
+                                            (d.far ? p.ws.far_ml : p.ws.own_ml))[place];
+        src = reinterpret_cast<const float*>(p.workspace + (d.far ? p.ws.far_o : p.ws.own_o)) +
+              place * DIM;
       }
     }
+    float t = v.x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, d));
+    if (lane == 0) red[0][warp] = t;
+    __syncthreads();
+    float now = top;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) now = fmaxf(now, red[0][w]);
+    const float base = now == -INFINITY ? 0.f : now;
+    const float keep = exp2f(top - base);
+    // A part without weight is not read (its values were not written).
+    const float f = v.y != 0.f ? exp2f(v.x - base) : 0.f;
+    weight[threadIdx.x] = f;
+    source[threadIdx.x] = f != 0.f ? src : nullptr;
+    float part = f * v.y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(kAll, part, d);
+    if (lane == 0) red[1][warp] = part;
+    __syncthreads();
+    sum *= keep;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) sum += red[1][w];
+    top = now;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= keep;
+    for (int j = warp; j < count; j += 4 * kJoinWarps) {
+      float x[4][E], fj[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int at = j + u * kJoinWarps;
+        const float* from = at < count ? source[at] : nullptr;
+        fj[u] = from ? weight[at] : 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[u][e] = 0.f;
+        if (from) {
+          if (E == 4) {
+            const float4 y = reinterpret_cast<const float4*>(from)[lane];
+            x[u][0] = y.x, x[u][1] = y.y, x[u][2 % E] = y.z, x[u][3 % E] = y.w;
+          } else {
+            const float2 y = reinterpret_cast<const float2*>(from)[lane];
+            x[u][0] = y.x, x[u][1] = y.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += fj[u] * x[u][e];
+    }
+    __syncthreads();
   }
+#pragma unroll
+  for (int e = 0; e < E; ++e) values[warp][lane * E + e] = acc[e];
+  __syncthreads();
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
   uint16_t* out = static_cast<uint16_t*>(p.out.data) + (int64_t)token * p.out.token_stride +
-                  (int64_t)head * p.out.head_stride + lane * E;
+                  (int64_t)head * p.out.head_stride;
+  if (threadIdx.x < DIM / 2) {
+    const int e = 2 * (int)threadIdx.x;
+    float lo = 0.f, hi = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(out + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-  if (p.lse && lane == 0)
-    p.lse[id] = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    for (int w = 0; w < kJoinWarps; ++w) lo += values[w][e], hi += values[w][e + 1];
+    *reinterpret_cast<uint32_t*>(out + e) = pack_bf16(lo * inv, hi * inv);
+  }
+  if (p.lse && threadIdx.x == 0)
+    p.lse[blockIdx.x] = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int DIM>
-cudaError_t launch_dim(const AttentionParams& p, const CUtensorMap& k_map,
-                       const CUtensorMap& v_map, cudaStream_t stream) {
+cudaError_t launch_dim(const AttentionParams& p, const PageMaps& maps, cudaStream_t stream) {
   static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1173,8 +1309,7 @@ cudaError_t launch_dim(const AttentionParams& p, const CUtensorMap& k_map,
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  const int64_t warps = (int64_t)p.batch.sequences * p.batch.chunk * p.heads;
-  const int64_t blocks = (warps + kJoinWarps - 1) / kJoinWarps;
+  const int64_t blocks = (int64_t)p.batch.sequences * p.batch.chunk * p.heads;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.ctas);
@@ -1186,10 +1321,10 @@ cudaError_t launch_dim(const AttentionParams& p, const CUtensorMap& k_map,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attention_kernel<DIM>, p, k_map, v_map);
+  e = cudaLaunchKernelEx(&cfg, attention_kernel<DIM>, p, maps);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel<DIM>, p);
 }
@@ -1204,10 +1339,15 @@ AttentionWorkspace attention_workspace(int sequences, int chunk, int groups, int
   const int64_t seq_rows = (int64_t)chunk * (heads / kv_heads);
   const int64_t far_items =
       groups ? ((seq_rows * sequences + kPairRows - 1) / kPairRows + groups) * kv_heads : 0;
-  w.own_rows = (int32_t)(seq_rows < kTeamRows ? seq_rows : kTeamRows);
-  w.own_items = (int32_t)((seq_rows + kPairRows - 1) / kPairRows * kv_heads);
-  w.far_slots = groups ? 2 * (far_items + ctas) : 0;
-  w.own_slots = 2 * ((int64_t)sequences * w.own_items + ctas);
+  const int few_heads = few_heads_of(kv_heads);
+  const bool few = seq_rows <= kFewRows;
+  w.seq_rows = few ? (int32_t)seq_rows : 0;
+  w.own_rows = (int32_t)(few ? seq_rows * (few_heads == 1 ? 2 : few_heads)
+                             : 2 * (seq_rows < kTeamRows ? seq_rows : kTeamRows));
+  w.own_items = (int32_t)(few ? kv_heads / few_heads
+                              : (seq_rows + kPairRows - 1) / kPairRows * kv_heads);
+  w.far_slots = groups ? far_items + ctas : 0;
+  w.own_slots = (int64_t)sequences * w.own_items + ctas;
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) {
     const uint64_t here = at;
@@ -1216,18 +1356,17 @@ AttentionWorkspace attention_workspace(int sequences, int chunk, int groups, int
   };
   w.starts = take(8ull * ((uint64_t)groups + sequences + 1));
   w.items = take(4ull * ((uint64_t)groups + 1));
-  w.far_ml = take(8ull * w.far_slots * kTeamRows);
-  w.far_o = take(4ull * w.far_slots * kTeamRows * dim);
+  w.far_ml = take(8ull * w.far_slots * kPairRows);
+  w.far_o = take(4ull * w.far_slots * kPairRows * dim);
   w.own_ml = take(8ull * w.own_slots * w.own_rows);
   w.own_o = take(4ull * w.own_slots * w.own_rows * dim);
   w.bytes = at;
   return w;
 }
 
-cudaError_t launch_attention(const AttentionParams& p, const CUtensorMap& k_map,
-                             const CUtensorMap& v_map, cudaStream_t stream) {
-  return p.dim == 64 ? launch_dim<64>(p, k_map, v_map, stream)
-                     : launch_dim<128>(p, k_map, v_map, stream);
+cudaError_t launch_attention(const AttentionParams& p, const PageMaps& maps,
+                             cudaStream_t stream) {
+  return p.dim == 64 ? launch_dim<64>(p, maps, stream) : launch_dim<128>(p, maps, stream);
 }
 
 }  // namespace nwc

@@ -77,16 +77,25 @@ cudaError_t launch_rope(const RopeParams& p, int in_type, int out_type, int sm_c
 constexpr int kKvTile = 128;
 constexpr int kTeamRows = 128;
 constexpr int kPairRows = 2 * kTeamRows;
+constexpr int kFewRows = 16;  // rows of a segment that are multiplied without TMEM
+// Heads that a tile of such a segment holds (16 tokens of one head a warp), so it
+// has 128 / that tokens: the largest power of two up to 8 that divides the heads.
+inline int few_heads_of(int kv_heads) {
+  int n = 8;
+  while (kv_heads % n) n /= 2;
+  return n;
+}
 
 // The workspace: where each segment's tiles and items start (segments + 1 each,
 // the last the totals), then the parts' results, prefixes' and own.
 struct AttentionWorkspace {
   uint64_t starts;        // int64 [segments + 1]: first tile
   uint64_t items;         // int32 [groups + 1]: first item of a prefix
-  uint64_t far_ml, far_o; // prefixes: float2 [slots][128], float [slots][128][dim]
+  uint64_t far_ml, far_o; // prefixes: float2 [slots][256], float [slots][256][dim]
   uint64_t own_ml, own_o; // own: the same with own_rows rows
   int64_t far_slots, own_slots;
-  int32_t own_rows;       // rows a slot of an own part holds
+  int32_t own_rows;       // rows a slot of an own part holds: both teams', or all heads'
+  int32_t seq_rows;       // rows of a sequence for a key head, where they are few
   int32_t own_items;      // items of a sequence's own segment
   uint64_t bytes;
 };
@@ -103,11 +112,15 @@ struct AttentionParams {
   uint8_t* workspace;
   AttentionWorkspace ws;
   int32_t ctas;
+  int32_t few_heads, few_tokens;  // of a tile of a segment of few rows
   uint32_t wait_limit;        // polls before a bounded wait gives up (0: default)
 };
-// k_map, v_map: the pages as [pages][kv_heads][page_size][dim], box 64 elements
-// x min(page_size, 128) tokens, 128-byte swizzle.
-cudaError_t launch_attention(const AttentionParams& p, const CUtensorMap& k_map,
-                             const CUtensorMap& v_map, cudaStream_t stream);
+// The pages of K and V as [pages][kv_heads][page_size][dim], 128-byte swizzle: with
+// a box of 64 elements x min(page_size, 128) tokens, then with one of 64 x
+// min(page_size, few_tokens) x few_heads.
+struct PageMaps {
+  CUtensorMap map[4];
+};
+cudaError_t launch_attention(const AttentionParams& p, const PageMaps& maps, cudaStream_t stream);
 
 }  // namespace nwc

@@ -129,15 +129,15 @@ nwc_status run_rope(const nwc::RopeParams& p, int in_type, int out_type, nwc_str
 // The TMA descriptor of a cache's K or V pages.  Strides of dimensions of one
 // element play no part but have to be valid.
 bool page_map(const nwc_kv_cache& c, uint16_t* base, int64_t page_stride, int64_t token_stride,
-              int64_t head_stride, CUtensorMap* map) {
+              int64_t head_stride, int tokens, int heads, CUtensorMap* map) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = nwc::tensor_map_encoder();
   if (!encode) return false;
-  const int32_t rows = c.page_size < nwc::kKvTile ? c.page_size : nwc::kKvTile;
+  const int32_t rows = c.page_size < tokens ? c.page_size : tokens;
   const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads,
                               (cuuint64_t)c.pages};
   const cuuint64_t strides[3] = {(cuuint64_t)token_stride * 2, (cuuint64_t)head_stride * 2,
                                  (cuuint64_t)page_stride * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)heads, 1};
   const cuuint32_t elem[4] = {1, 1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, elem,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -242,14 +242,19 @@ nwc_status nwc_kv_attention(const nwc_kv_cache* cache, const nwc_kv_batch* batch
   p.batch = view(*batch);
   p.workspace = static_cast<uint8_t*>(d_workspace);
   p.wait_limit = nwc::wait_limit();
-  CUtensorMap k_map, v_map;
-  if (!page_map(*cache, cache->d_k, cache->k_page_stride, cache->k_token_stride,
-                cache->k_head_stride, &k_map) ||
-      !page_map(*cache, cache->d_v, cache->v_page_stride, cache->v_token_stride,
-                cache->v_head_stride, &v_map))
-    return NWC_ERR_UNSUPPORTED;
-  return nwc::launch_attention(p, k_map, v_map, reinterpret_cast<cudaStream_t>(stream)) ==
-                 cudaSuccess
+  p.few_heads = nwc::few_heads_of(cache->kv_heads);
+  p.few_tokens = nwc::kKvTile / p.few_heads;
+  nwc::PageMaps maps;
+  for (int i = 0; i < 4; ++i) {
+    const int tokens = i < 2 ? nwc::kKvTile : p.few_tokens, per = i < 2 ? 1 : p.few_heads;
+    const bool ok =
+        i % 2 == 0 ? page_map(*cache, cache->d_k, cache->k_page_stride, cache->k_token_stride,
+                              cache->k_head_stride, tokens, per, &maps.map[i])
+                   : page_map(*cache, cache->d_v, cache->v_page_stride, cache->v_token_stride,
+                              cache->v_head_stride, tokens, per, &maps.map[i]);
+    if (!ok) return NWC_ERR_UNSUPPORTED;
+  }
+  return nwc::launch_attention(p, maps, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? NWC_OK
              : NWC_ERR_CUDA;
 }

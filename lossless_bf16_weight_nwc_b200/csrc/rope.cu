@@ -109,7 +109,7 @@ __device__ __forceinline__ Place place_of(const CacheView& c, const BatchView& b
   at.slot_page = -1;
   if (at.real) {
     const int n = j >> c.page_shift;
-    if (n < b.table_width) at.slot_page = b.table[(int64_t)seq * b.table_stride + n];
+    if (n < b.table_width && j < (1 << 30)) at.slot_page = b.table[(int64_t)seq * b.table_stride + n];
     if (at.slot_page < 0 || at.slot_page >= c.pages) {
       at.slot_page = -1;
       if (lane == 0) atomicOr(c.err, kErrRange);
