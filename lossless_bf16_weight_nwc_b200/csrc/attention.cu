@@ -71,6 +71,8 @@ struct Part {
   int32_t kvh;     // key head, or the first of kFew's
   int32_t tile0;   // tiles [tile0, tile0 + n) of the segment
   int64_t place;   // first row of its results; negative: none
+  int32_t* spans;  // its item's first and last CTA
+  bool first, last;  // whether this is the one
 };
 struct Announced {
   Part part;
@@ -158,16 +160,13 @@ __device__ __forceinline__ Segment segment(const AttentionParams& p, int s) {
   r.lead = r.few ? kLeadFew : r.rows <= kTeamRows ? kLeadOne : kLeadBoth;
   return r;
 }
-// The tiles lie on an axis of costs; of `ctas` CTAs, c has those that start in
+// The tiles lie on an axis of costs; of the CTAs that share it, c has those that start in
 // [share(c), share(c + 1)).  (Divisions of 64 bits are long: 32 where they do.)
 __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 __device__ __forceinline__ int64_t share(int64_t total, int c, int ctas) {
   return divide(total * c, ctas);
-}
-__device__ __forceinline__ int owner(int64_t total, int64_t at, int ctas) {
-  return (int)divide((at + 1) * ctas - 1, total);
 }
 
 // The slot of a part's results: item + CTA is different for any two parts, as
@@ -178,6 +177,13 @@ __device__ __forceinline__ int64_t slot_of(const AttentionParams& p, int s, int 
           ? reinterpret_cast<const int32_t*>(p.workspace + p.ws.items)[s]
           : (int64_t)(s - p.batch.groups) * p.ws.own_items;
   return first + item + cta;
+}
+
+// The first and last CTA of an item (counted over the prefixes' or over the own).
+__device__ __forceinline__ int32_t* spans_of(const AttentionParams& p, int s, int64_t item) {
+  return reinterpret_cast<int32_t*>(p.workspace +
+                                    (s < p.batch.groups ? p.ws.far_spans : p.ws.own_spans)) +
+         2 * item;
 }
 
 // A segment's items on the axis: each a lead, then its tiles.
@@ -224,6 +230,9 @@ struct Walk {
       const int64_t slot = slot_of(p, s, item, (int)blockIdx.x);
       const bool room = slot < (g.far ? p.ws.far_slots : p.ws.own_slots);
       part.place = room ? slot * (g.far ? kPairRows : p.ws.own_rows) : -1;
+      part.spans = spans_of(p, s, slot - blockIdx.x);
+      part.first = part.tile0 == 0;
+      part.last = part.tile0 + part.n == g.tiles;
       tile += part.n;
       return true;
     }
@@ -306,7 +315,12 @@ __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* maps, ui
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(&bars->told[e]);
-      if (more && part.place < 0) atomicOr(p.cache.err, kErrRange);
+      if (more && part.place < 0) {
+        atomicOr(p.cache.err, kErrRange);
+      } else if (more) {
+        if (part.first) part.spans[0] = (int32_t)blockIdx.x;
+        if (part.last) part.spans[1] = (int32_t)blockIdx.x;
+      }
     }
     if (!more) break;
     const int32_t* row = part.far ? b.prefix_table + (int64_t)walk.s * b.prefix_stride
@@ -988,35 +1002,46 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
   }
 }
 
+// This CTA's share of the axis.  A share is at least as long as the widest gap
+// between two tiles' starts, so that no CTA among an item's is without a tile.
+__device__ __forceinline__ void share_of(const AttentionParams& p, int64_t total, bool many,
+                                         int64_t* from, int64_t* to) {
+  const int gap = many ? kCostBoth + kLeadBoth : kCostFew + kLeadFew;
+  const int ctas = (int)min((int64_t)p.ctas, max(divide(total, gap), (int64_t)1));
+  const int c = (int)blockIdx.x;
+  *from = c < ctas ? share(total, c, ctas) : total;
+  *to = c < ctas ? share(total, c + 1, ctas) : total;
+}
+
 // First tile and first item of every segment, by a scan of the whole CTA; finds
-// this CTA's share.  CTA 0 writes the starts down for the kernel that joins the
-// parts, and reports lengths that the tables do not hold.
+// this CTA's share.  CTA 0 reports lengths that the tables do not hold.
 __device__ Walk share_out(const AttentionParams& p, Bars* bars) {
   const BatchView& b = p.batch;
   const int segments = b.groups + b.sequences;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t* starts = reinterpret_cast<int64_t*>(p.workspace + p.ws.starts);
   int32_t* items = reinterpret_cast<int32_t*>(p.workspace + p.ws.items);
   const int chunks = (segments + kThreads - 1) / kThreads;
   int64_t run = 0, f0 = -1, f1 = 0;
   int32_t run_items = 0;
+  bool many = false;   // a segment that is not of few rows
   // Up to kThreads segments at a time for the total, then once more (unless there
   // is but one time) to find the segment of the share's start.
 #pragma unroll 1
   for (int turn = 0; turn < 2 * chunks - (chunks == 1); ++turn) {
     if (turn == chunks) {
-      f0 = share(run, (int)blockIdx.x, p.ctas);
-      f1 = share(run, (int)blockIdx.x + 1, p.ctas);
+      share_of(p, run, many, &f0, &f1);
       run = 0;
       run_items = 0;
     }
     const int s = (turn < chunks ? turn : turn - chunks) * kThreads + (int)threadIdx.x;
     int32_t n = 0;
     int64_t flat = 0;
+    bool any = false;
     if (s < segments) {
       const Segment g = segment(p, s);
       flat = item_span(g) * g.items;
       n = g.items;
+      any = !g.few && flat > 0;
     }
     int64_t f = flat;
     int32_t m = n;
@@ -1026,7 +1051,7 @@ __device__ Walk share_out(const AttentionParams& p, Bars* bars) {
       const int32_t m2 = __shfl_up_sync(kAll, m, o);
       if (lane >= o) f += f2, m += m2;
     }
-    __syncthreads();
+    many |= __syncthreads_or(any) != 0;
     if (lane == 31) bars->warp_flat[warp] = f, bars->warp_items[warp] = m;
     __syncthreads();
     int64_t before = run + f - flat;
@@ -1037,16 +1062,12 @@ __device__ Walk share_out(const AttentionParams& p, Bars* bars) {
       run += bars->warp_flat[k];
       run_items += bars->warp_items[k];
     }
-    if (chunks == 1) {
-      f0 = share(run, (int)blockIdx.x, p.ctas);
-      f1 = share(run, (int)blockIdx.x + 1, p.ctas);
-    }
+    if (chunks == 1) share_of(p, run, many, &f0, &f1);
     if (s < segments) {
       // Every CTA needs its prefixes' first items for its slots: all write the
       // same values.
       if (s < b.groups) items[s] = before_items;
       if (blockIdx.x == 0 && turn < chunks) {
-        starts[s] = before;
         const int len = s < b.groups ? b.prefix_lens[s] : b.lens[s - b.groups];
         if (len > (s < b.groups ? far_len(p, s) : own_len(p, s - b.groups)) && len > 0)
           atomicOr(p.cache.err, kErrRange);
@@ -1054,7 +1075,6 @@ __device__ Walk share_out(const AttentionParams& p, Bars* bars) {
       if (before <= f0 && f0 < before + flat) bars->seg = s, bars->start = before;
     }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) starts[segments] = run;
   __syncthreads();
   Walk walk;
   walk.s = 0;
@@ -1132,14 +1152,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinWarps = 4;
 constexpr int kJoinThreads = kJoinWarps * 32;
 
-// Where a row's results lie in a segment's parts.
+// Where a row's results lie in a segment's parts: for k < n in row place + k / teams *
+// part_rows + k % teams * team_rows (a part has the row once, or for each of the
+// two teams that share it).
 struct Side {
-  int64_t t0;      // where its item's first tile starts on the axis
-  int s, item, cost, c0;
-  int n, teams;    // results: CTAs from c0 on, times teams that have the row each
-  int at, team_rows, part_rows;
-  bool far;
+  int64_t place;
+  int n, teams, team_rows, part_rows;
 };
+__device__ __forceinline__ Side side_of(const AttentionParams& p, bool far, int rows, int row,
+                                        int kvh, int64_t first_item) {
+  Side d;
+  const bool few = rows <= kFewRows;
+  const int block = row / kPairRows, in_block = row - block * kPairRows;
+  const bool both = !few && min(rows - block * kPairRows, kPairRows) > kTeamRows;
+  const int in_heads = few ? kvh % p.few_heads : 0;
+  const int64_t item = first_item + (few ? kvh / p.few_heads : block * p.kv_heads + kvh);
+  d.teams = few ? (p.few_heads == 1 ? 2 : 1) : both ? 1 : 2;
+  d.team_rows = few ? (far ? kFewRows : p.ws.seq_rows) : far ? kTeamRows : p.ws.own_rows / 2;
+  d.part_rows = far ? kPairRows : p.ws.own_rows;
+  const int at = few    ? (p.few_heads == 1 ? 0 : in_heads) * d.team_rows + row
+                 : both ? in_block / kTeamRows * d.team_rows + in_block % kTeamRows
+                        : in_block;
+  d.n = 0;
+  d.place = 0;
+  const int64_t slots = far ? p.ws.far_slots : p.ws.own_slots;
+  if (item < slots - p.ctas) {
+    const int2 span = *reinterpret_cast<const int2*>(
+        p.workspace + (far ? p.ws.far_spans : p.ws.own_spans) + 8 * item);
+    d.n = (span.y - span.x + 1) * d.teams;
+    d.place = (item + span.x) * d.part_rows + at;
+  }
+  return d;
+}
 
 // One CTA a row and query head: over the parts of its prefix and its own tokens,
 // out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i, in a fixed order.  A thread a
@@ -1155,53 +1199,39 @@ __global__ void __launch_bounds__(kJoinThreads)
   allow_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const BatchView& b = p.batch;
-  const int token = (int)(blockIdx.x / (unsigned)p.heads);
-  const int head = (int)(blockIdx.x - (unsigned)token * (unsigned)p.heads);
-  const int seq = token / b.chunk, i = token - seq * b.chunk;
+  const int token = (int)blockIdx.x, head = (int)blockIdx.y;
+  const int seq = b.chunk == 1 ? token : token / b.chunk, i = token - seq * b.chunk;
   const int gq = p.heads / p.kv_heads, kvh = head / gq, h = head - kvh * gq;
+  const int in_seq = i * gq + h, seq_rows = b.chunk * gq;
   wait_prerequisites();
-  const int64_t* starts = reinterpret_cast<const int64_t*>(p.workspace + p.ws.starts);
-  const int64_t total = starts[b.groups + b.sequences];
-  int group = -1;
-  for (int g0 = 0; g0 < b.groups; g0 += 32) {
-    const int g = g0 + lane;
-    const bool in = g < b.groups && b.group_start[g] <= seq && seq < b.group_start[g + 1];
-    const unsigned hit = __ballot_sync(kAll, in);
-    if (hit) {
-      group = g0 + __ffs(hit) - 1;
-      break;
+  Side far, own;
+  far.n = own.n = 0;
+  const int fresh = fresh_of(b, seq);
+  if (i < fresh) {
+    if (own_len(p, seq) > 0)
+      own = side_of(p, false, seq_rows, in_seq, kvh, (int64_t)seq * p.ws.own_items);
+    for (int g0 = 0; g0 < b.groups; g0 += 32) {
+      const int g = g0 + lane;
+      int first = 0, end = 0, len = 0, item = 0;
+      if (g < b.groups) {
+        first = b.group_start[g];
+        end = b.group_start[g + 1];
+        len = b.prefix_lens[g];
+        item = reinterpret_cast<const int32_t*>(p.workspace + p.ws.items)[g];
+      }
+      const unsigned hit = __ballot_sync(kAll, first <= seq && seq < end);
+      if (hit) {
+        const int from = __ffs(hit) - 1;
+        first = max(__shfl_sync(kAll, first, from), 0);
+        end = min(__shfl_sync(kAll, end, from), b.sequences);
+        item = __shfl_sync(kAll, item, from);
+        if (__shfl_sync(kAll, len, from) > 0)
+          far = side_of(p, true, (end - first) * seq_rows, (seq - first) * seq_rows + in_seq, kvh,
+                        item);
+        break;
+      }
     }
   }
-  const bool real = i < fresh_of(b, seq);
-  auto side_of = [&](int s) {
-    Side d;
-    d.n = 0;
-    if (!real || s < 0) return d;
-    const Segment seg = segment(p, s);
-    if (seg.tiles == 0) return d;
-    const int row = ((seq - seg.seq0) * b.chunk + i) * gq + h;
-    const int block = row / kPairRows, in_block = row - block * kPairRows;
-    const bool both = !seg.few && min(seg.rows - block * kPairRows, kPairRows) > kTeamRows;
-    d.s = s;
-    d.far = seg.far;
-    d.cost = seg.cost;
-    d.item = seg.few ? kvh / p.few_heads : block * p.kv_heads + kvh;
-    d.t0 = starts[s] + item_span(seg) * d.item + seg.lead;
-    d.c0 = owner(total, d.t0, p.ctas);
-    // A part has the row once, or for each of the two teams that share it.
-    d.teams = seg.few ? (p.few_heads == 1 ? 2 : 1) : both ? 1 : 2;
-    d.n = (owner(total, d.t0 + (int64_t)(seg.tiles - 1) * seg.cost, p.ctas) - d.c0 + 1) *
-          d.teams;
-    d.team_rows = seg.few  ? (seg.far ? kFewRows : p.ws.seq_rows)
-                  : seg.far ? kTeamRows
-                            : p.ws.own_rows / 2;
-    d.at = seg.few ? (p.few_heads == 1 ? 0 : kvh % p.few_heads) * d.team_rows + row
-           : both  ? in_block / kTeamRows * d.team_rows + in_block % kTeamRows
-                   : in_block;
-    d.part_rows = seg.far ? kPairRows : p.ws.own_rows;
-    return d;
-  };
-  const Side far = side_of(group), own = side_of(b.groups + seq);
   float top = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -1211,22 +1241,16 @@ __global__ void __launch_bounds__(kJoinThreads)
     const float* src = nullptr;
     if ((int)threadIdx.x < count) {
       const bool in_far = k0 + (int)threadIdx.x < far.n;
-      const Side& d = in_far ? far : own;
       const int k = k0 + (int)threadIdx.x - (in_far ? 0 : far.n);
-      const int cta = d.c0 + k / d.teams;
-      // Where a tile costs more than a share, a CTA between may have none.
-      const int64_t from = share(total, cta, p.ctas);
-      const int64_t tile =
-          from > d.t0 ? d.t0 + divide(from - d.t0 + d.cost - 1, d.cost) * d.cost : d.t0;
-      const int64_t slot = slot_of(p, d.s, d.item, cta);
-      const int64_t place = slot * d.part_rows + k % d.teams * d.team_rows + d.at;
-      if (slot < (d.far ? p.ws.far_slots : p.ws.own_slots) &&
-          tile < share(total, cta + 1, p.ctas)) {
-        v = reinterpret_cast<const float2*>(p.workspace +
-                                            (d.far ? p.ws.far_ml : p.ws.own_ml))[place];
-        src = reinterpret_cast<const float*>(p.workspace + (d.far ? p.ws.far_o : p.ws.own_o)) +
-              place * DIM;
-      }
+      const int part = (in_far ? far.teams : own.teams) == 2 ? k >> 1 : k;
+      const int team = (in_far ? far.teams : own.teams) == 2 ? k & 1 : 0;
+      const int64_t place = (in_far ? far.place : own.place) +
+                            (int64_t)part * (in_far ? far.part_rows : own.part_rows) +
+                            team * (in_far ? far.team_rows : own.team_rows);
+      v = reinterpret_cast<const float2*>(p.workspace +
+                                          (in_far ? p.ws.far_ml : p.ws.own_ml))[place];
+      src = reinterpret_cast<const float*>(p.workspace + (in_far ? p.ws.far_o : p.ws.own_o)) +
+            place * DIM;
     }
     float t = v.x;
 #pragma unroll
@@ -1293,7 +1317,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     *reinterpret_cast<uint32_t*>(out + e) = pack_bf16(lo * inv, hi * inv);
   }
   if (p.lse && threadIdx.x == 0)
-    p.lse[blockIdx.x] = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    p.lse[(int64_t)token * p.heads + head] = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int DIM>
@@ -1309,8 +1333,6 @@ cudaError_t launch_dim(const AttentionParams& p, const PageMaps& maps, cudaStrea
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  const int64_t blocks = (int64_t)p.batch.sequences * p.batch.chunk * p.heads;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.ctas);
   cfg.blockDim = dim3(kThreads);
@@ -1323,7 +1345,8 @@ cudaError_t launch_dim(const AttentionParams& p, const PageMaps& maps, cudaStrea
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attention_kernel<DIM>, p, maps);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim =
+      dim3((unsigned)(p.batch.sequences * p.batch.chunk), (unsigned)p.heads);  // <= 2^24, 2^12
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel<DIM>, p);
@@ -1354,7 +1377,8 @@ AttentionWorkspace attention_workspace(int sequences, int chunk, int groups, int
     at += up256(bytes);
     return here;
   };
-  w.starts = take(8ull * ((uint64_t)groups + sequences + 1));
+  w.far_spans = take(8ull * far_items);
+  w.own_spans = take(8ull * sequences * w.own_items);
   w.items = take(4ull * ((uint64_t)groups + 1));
   w.far_ml = take(8ull * w.far_slots * kPairRows);
   w.far_o = take(4ull * w.far_slots * kPairRows * dim);

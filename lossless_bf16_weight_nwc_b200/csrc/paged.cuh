@@ -86,10 +86,10 @@ inline int few_heads_of(int kv_heads) {
   return n;
 }
 
-// The workspace: where each segment's tiles and items start (segments + 1 each,
-// the last the totals), then the parts' results, prefixes' and own.
+// The workspace: which CTAs have an item's parts, then the parts' results,
+// prefixes' and own.
 struct AttentionWorkspace {
-  uint64_t starts;        // int64 [segments + 1]: first tile
+  uint64_t far_spans, own_spans;  // int32 [items][2]: first and last CTA
   uint64_t items;         // int32 [groups + 1]: first item of a prefix
   uint64_t far_ml, far_o; // prefixes: float2 [slots][256], float [slots][256][dim]
   uint64_t own_ml, own_o; // own: the same with own_rows rows
