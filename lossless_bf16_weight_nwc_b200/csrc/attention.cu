@@ -93,10 +93,6 @@ struct Bars {
   uint64_t drain;
   uint32_t tmem;
   uint32_t abort;
-  int32_t seg;               // the segment in which this CTA's share starts
-  int64_t start;             // and its place on the axis
-  int64_t warp_flat[kThreads / 32];
-  int32_t warp_items[kThreads / 32];
   float2 ml[2][4][kFewRows]; // maximum and sum of each warp's rows in a part of few rows
   Announced queue[kQueue];
 };
@@ -113,15 +109,18 @@ struct Segment {
   int tiles;
   int items;
   bool few;    // at most kFewRows rows
+  Kind kind;   // of its first block of rows
   int cost;    // of a tile on the axis that is shared out
   int lead;    // of an item's start
   bool far;    // a prefix
 };
 
-// What a tile costs by the rows of its segment, and what each item adds at its start
-// (a part's beginning and end), in about 1000 cycles.
-constexpr int kCostFew = 2, kCostOne = 3, kCostBoth = 5;
-constexpr int kLeadFew = 2, kLeadOne = 6, kLeadBoth = 10;
+// What a tile costs by the kind of its segment, and what each item adds at its start
+// (a part's end and the next one's beginning), in units of about 400 cycles: fitted
+// to the times of CTAs with different parts (heads of 64, then of 128).
+__device__ constexpr int kCost[2][3] = {{3, 6, 9}, {4, 9, 10}};
+__device__ constexpr int kLead[2][3] = {{8, 7, 14}, {9, 8, 33}};
+constexpr int kCostMost = 10;
 
 __device__ __forceinline__ int fresh_of(const BatchView& b, int seq) {
   return b.q_lens ? min(max(b.q_lens[seq], 0), b.chunk) : b.chunk;
@@ -134,30 +133,34 @@ __device__ __forceinline__ int far_len(const AttentionParams& p, int g) {
   const int64_t cap = min((int64_t)p.batch.prefix_width << p.cache.page_shift, kMaxTokens);
   return (int)min((int64_t)max(p.batch.prefix_lens[g], 0), cap);
 }
-__device__ __forceinline__ Segment segment(const AttentionParams& p, int s) {
+// cap: the most that an item's lead may cost; negative: every tile costs 1 and a
+// lead nothing.  (No divisions here: a part's announcement is on the way to its first
+// byte.)
+__device__ __forceinline__ Segment segment(const AttentionParams& p, int s, int cap) {
   const BatchView& b = p.batch;
   Segment r;
-  const int gq = p.heads / p.kv_heads;
   if (s < b.groups) {
     r.far = true;
     r.seq0 = min(max(b.group_start[s], 0), b.sequences);
     const int end = min(max(b.group_start[s + 1], r.seq0), b.sequences);
-    r.rows = (end - r.seq0) * b.chunk * gq;
-    r.len = r.rows ? far_len(p, s) : 0;
+    r.rows = (end - r.seq0) * p.seq_rows;
+    r.len = far_len(p, s);
+    if (r.rows == 0) r.len = 0;
   } else {
     r.far = false;
     r.seq0 = s - b.groups;
-    r.rows = b.chunk * gq;
-    r.len = fresh_of(b, r.seq0) ? own_len(p, r.seq0) : 0;
+    r.rows = p.seq_rows;
+    r.len = own_len(p, r.seq0);
+    if (b.q_lens && b.q_lens[r.seq0] <= 0) r.len = 0;
   }
   r.few = r.rows <= kFewRows;
-  // Not (len + tile - 1) / tile, which may pass 31 bits.
-  const int tile = r.few ? p.few_tokens : kKvTile;
-  r.tiles = r.len / tile + (r.len % tile != 0);
-  r.items = r.few ? p.kv_heads / p.few_heads * (r.rows > 0)
+  const int shift = r.few ? p.few_shift : kKvShift;
+  r.tiles = (int)(((uint32_t)r.len + (1u << shift) - 1) >> shift);
+  r.items = r.few ? (r.rows > 0 ? p.few_items : 0)
                   : (r.rows + kPairRows - 1) / kPairRows * p.kv_heads;
-  r.cost = r.few ? kCostFew : r.rows <= kTeamRows ? kCostOne : kCostBoth;
-  r.lead = r.few ? kLeadFew : r.rows <= kTeamRows ? kLeadOne : kLeadBoth;
+  r.kind = r.few ? kFew : r.rows <= kTeamRows ? kOne : kBoth;
+  r.cost = cap < 0 ? 1 : kCost[p.dim == 128][r.kind];
+  r.lead = cap < 0 ? 0 : min(kLead[p.dim == 128][r.kind], cap);
   return r;
 }
 // The tiles lie on an axis of costs; of the CTAs that share it, c has those that start in
@@ -167,16 +170,6 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 }
 __device__ __forceinline__ int64_t share(int64_t total, int c, int ctas) {
   return divide(total * c, ctas);
-}
-
-// The slot of a part's results: item + CTA is different for any two parts, as
-// each next part has a later item, a later CTA or both.
-__device__ __forceinline__ int64_t slot_of(const AttentionParams& p, int s, int item, int cta) {
-  const int64_t first =
-      s < p.batch.groups
-          ? reinterpret_cast<const int32_t*>(p.workspace + p.ws.items)[s]
-          : (int64_t)(s - p.batch.groups) * p.ws.own_items;
-  return first + item + cta;
 }
 
 // The first and last CTA of an item (counted over the prefixes' or over the own).
@@ -200,12 +193,13 @@ __device__ __forceinline__ int64_t tile_from(const Segment& g, int64_t at) {
 // The parts of a CTA in order: those of the tiles that start in [from, to) of the
 // axis, from segment s, which starts at `start`; `tile`, the first one left of it.
 struct Walk {
-  int s;
+  int s, cap;
   int64_t start, from, to, tile;
+  int64_t item0;   // the segment's first item, counted over the prefixes' or the own
   __device__ __forceinline__ bool next(const AttentionParams& p, Part& part) {
     const int segments = p.batch.groups + p.batch.sequences;
     while (s < segments && start < to) {
-      const Segment g = segment(p, s);
+      const Segment g = segment(p, s, cap);
       const int64_t span = item_span(g) * g.items;
       if (tile < 0 && span > 0) tile = from > start ? tile_from(g, from - start) : 0;
       const int64_t end =
@@ -213,7 +207,7 @@ struct Walk {
       if (tile >= end || span == 0) {
         start += span;
         tile = -1;
-        ++s;
+        item0 = ++s == p.batch.groups ? 0 : item0 + g.items;
         continue;
       }
       const int item = (int)divide(tile, g.tiles);
@@ -227,10 +221,12 @@ struct Walk {
       part.far = g.far;
       part.seq0 = g.seq0;
       part.len = g.len;
-      const int64_t slot = slot_of(p, s, item, (int)blockIdx.x);
+      // The slot of its results: item + CTA is different for any two parts, as each
+      // next part has a later item, a later CTA or both.
+      const int64_t slot = item0 + item + blockIdx.x;
       const bool room = slot < (g.far ? p.ws.far_slots : p.ws.own_slots);
       part.place = room ? slot * (g.far ? kPairRows : p.ws.own_rows) : -1;
-      part.spans = spans_of(p, s, slot - blockIdx.x);
+      part.spans = spans_of(p, s, item0 + item);
       part.first = part.tile0 == 0;
       part.last = part.tile0 + part.n == g.tiles;
       tile += part.n;
@@ -271,12 +267,12 @@ struct Row {
 };
 __device__ __forceinline__ Row row_of(const AttentionParams& p, const Part& part, int r) {
   const BatchView& b = p.batch;
-  const int gq = p.heads / p.kv_heads, per = b.chunk * gq, at = part.base + r;
-  const int sl = at / per, rest = at - sl * per, i = rest / gq;
+  const int at = part.base + r;
+  const int sl = at / p.seq_rows, rest = at - sl * p.seq_rows, i = rest / p.gq;
   const int seq = part.seq0 + sl, fresh = fresh_of(b, seq);
   Row row;
   row.q = (int64_t)(seq * b.chunk + i) * p.q.token_stride +
-          (int64_t)(part.kvh * gq + rest - i * gq) * p.q.head_stride;
+          (int64_t)(part.kvh * p.gq + rest - i * p.gq) * p.q.head_stride;
   row.limit = 0;
   if (i < fresh)
     row.limit =
@@ -284,17 +280,155 @@ __device__ __forceinline__ Row row_of(const AttentionParams& p, const Part& part
   return row;
 }
 
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// Where this CTA's share of the axis starts: the producer warp sums the segments,
+// four consecutive ones a lane, for the totals, then for the segment in which the
+// share starts (from registers where there are up to 128).  Of an item's CTAs none
+// may be without a tile (the join counts on it), so a share is at least as long as
+// the widest gap between two tiles' starts, the most that a tile costs plus a lead:
+// leads are capped for it, and where that leaves none every tile costs 1.
+__device__ Walk share_out(const AttentionParams& p) {
+  const BatchView& b = p.batch;
+  const int segments = b.groups + b.sequences;
+  const int lane = threadIdx.x & 31;
+  const int chunks = (segments + 127) / 128;
+  Segment g[4];
+  auto take = [&](int s0, int cap) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      g[j].tiles = g[j].items = 0;
+      g[j].kind = kFew;
+      if (s0 + j < segments) g[j] = segment(p, s0 + j, cap);
+    }
+  };
+  int64_t tiles = 0, cost = 0, of_kind[3] = {0, 0, 0};   // items of each kind
+#pragma unroll 1
+  for (int t = 0; t < chunks; ++t) {
+    const int s0 = t * 128 + 4 * lane;
+    take(s0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t all = (int64_t)g[j].tiles * g[j].items;
+      if (all == 0) continue;
+      tiles += all;
+      cost += all * g[j].cost;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) of_kind[k] += g[j].kind == k ? g[j].items : 0;
+    }
+  }
+  tiles = warp_sum(tiles);
+  cost = warp_sum(cost);
+  Walk walk;
+  const int64_t each = divide(cost, p.ctas) - kCostMost;
+  walk.cap = each < 0 ? -1 : (int)min(each, (int64_t)1024);
+  int64_t total = walk.cap < 0 ? tiles : cost;
+  if (walk.cap >= 0) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) total += warp_sum(of_kind[k]) * min(kLead[p.dim == 128][k], walk.cap);
+  }
+  const int ctas = (int)min((int64_t)p.ctas, max(total, (int64_t)1));
+  const int c = (int)blockIdx.x;
+  walk.from = c < ctas ? share(total, c, ctas) : total;
+  walk.to = c < ctas ? share(total, c + 1, ctas) : total;
+  walk.s = segments;
+  walk.start = walk.item0 = 0;
+  walk.tile = -1;
+  int64_t run = 0;
+  int32_t run_items = 0;
+#pragma unroll 1
+  for (int t = 0; t < chunks && run <= walk.from; ++t) {
+    const int s0 = t * 128 + 4 * lane;
+    if (chunks > 1) take(s0, walk.cap);
+    int64_t span[4], sum = 0;
+    int32_t n = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      g[j].cost = walk.cap < 0 ? 1 : kCost[p.dim == 128][g[j].kind];
+      g[j].lead = walk.cap < 0 ? 0 : min(kLead[p.dim == 128][g[j].kind], walk.cap);
+      span[j] = item_span(g[j]) * g[j].items;
+      sum += span[j];
+      n += g[j].items;
+    }
+    int64_t at = sum;
+    int32_t item0 = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t a = __shfl_up_sync(kAll, at, o);
+      const int32_t e = __shfl_up_sync(kAll, item0, o);
+      if (lane >= o) at += a, item0 += e;
+    }
+    const int64_t chunk = __shfl_sync(kAll, at, 31);
+    const int32_t chunk_items = __shfl_sync(kAll, item0, 31);
+    at += run - sum;
+    item0 += run_items - n;
+    int mine = -1;
+    int64_t start = 0, first = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (at <= walk.from && walk.from < at + span[j]) mine = s0 + j, start = at, first = item0;
+      at += span[j];
+      item0 += g[j].items;
+    }
+    const unsigned hit = __ballot_sync(kAll, mine >= 0);
+    if (hit) {
+      const int from = __ffs(hit) - 1;
+      walk.s = __shfl_sync(kAll, mine, from);
+      walk.start = __shfl_sync(kAll, start, from);
+      walk.item0 = __shfl_sync(kAll, first, from);
+    }
+    run += chunk;
+    run_items += chunk_items;
+  }
+  if (walk.s >= b.groups) walk.item0 = (int64_t)(walk.s - b.groups) * p.ws.own_items;
+  return walk;
+}
+// What the last CTA notes while its tiles come: prefixes' first items, lengths that
+// the tables do not hold.
+__device__ __noinline__ void note_segments(const AttentionParams& p) {
+  const BatchView& b = p.batch;
+  const int lane = threadIdx.x & 31;
+  int32_t* items = reinterpret_cast<int32_t*>(p.workspace + p.ws.items);
+  int32_t run = 0;
+  bool over = false;
+  for (int s0 = 0; s0 < b.groups + b.sequences; s0 += 32) {
+    const int s = s0 + lane;
+    int32_t n = 0;
+    if (s < b.groups) {
+      n = segment(p, s, 0).items;
+      over |= b.prefix_lens[s] > 0 && b.prefix_lens[s] > far_len(p, s);
+    } else if (s < b.groups + b.sequences) {
+      const int len = b.lens[s - b.groups];
+      over |= len > 0 && len > own_len(p, s - b.groups);
+    }
+    int32_t sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t e = __shfl_up_sync(kAll, sum, o);
+      if (lane >= o) sum += e;
+    }
+    if (s < b.groups) items[s] = run + sum - n;
+    run += __shfl_sync(kAll, sum, 31);
+  }
+  if (over) atomicOr(p.cache.err, kErrRange);
+}
+
 // Announces part after part and brings its tiles: K at place 2n of the ring's
 // sequence, V at 2n + 1.
 template <int DIM>
 __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* maps, uint8_t* smem,
-                           Bars* bars, Walk walk, const Ctl& ctl) {
+                           Bars* bars, const Ctl& ctl) {
   using L = Layout<DIM>;
   constexpr int kHalves = DIM / 64;
   const int lane = threadIdx.x & 31;
   const int page = 1 << p.cache.page_shift;
   const int mine = lane / kHalves, half = lane % kHalves;   // this lane's box and half of it
   const BatchView& b = p.batch;
+  Walk walk = share_out(p);
   uint32_t seq = 0;
   bool ok = true;
   for (uint32_t k = 0; ok; ++k) {
@@ -567,7 +701,7 @@ __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* sm
   for (int n = 0; n < G; ++n) {
     src[n] = 8 * n + g < part.rows
                  ? static_cast<const uint16_t*>(p.q.data) + told.q[8 * n + g] +
-                       (int64_t)(hd * (p.heads / p.kv_heads)) * p.q.head_stride
+                       (int64_t)(hd * p.gq) * p.q.head_stride
                  : nullptr;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -1002,92 +1136,6 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
   }
 }
 
-// This CTA's share of the axis.  A share is at least as long as the widest gap
-// between two tiles' starts, so that no CTA among an item's is without a tile.
-__device__ __forceinline__ void share_of(const AttentionParams& p, int64_t total, bool many,
-                                         int64_t* from, int64_t* to) {
-  const int gap = many ? kCostBoth + kLeadBoth : kCostFew + kLeadFew;
-  const int ctas = (int)min((int64_t)p.ctas, max(divide(total, gap), (int64_t)1));
-  const int c = (int)blockIdx.x;
-  *from = c < ctas ? share(total, c, ctas) : total;
-  *to = c < ctas ? share(total, c + 1, ctas) : total;
-}
-
-// First tile and first item of every segment, by a scan of the whole CTA; finds
-// this CTA's share.  CTA 0 reports lengths that the tables do not hold.
-__device__ Walk share_out(const AttentionParams& p, Bars* bars) {
-  const BatchView& b = p.batch;
-  const int segments = b.groups + b.sequences;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int32_t* items = reinterpret_cast<int32_t*>(p.workspace + p.ws.items);
-  const int chunks = (segments + kThreads - 1) / kThreads;
-  int64_t run = 0, f0 = -1, f1 = 0;
-  int32_t run_items = 0;
-  bool many = false;   // a segment that is not of few rows
-  // Up to kThreads segments at a time for the total, then once more (unless there
-  // is but one time) to find the segment of the share's start.
-#pragma unroll 1
-  for (int turn = 0; turn < 2 * chunks - (chunks == 1); ++turn) {
-    if (turn == chunks) {
-      share_of(p, run, many, &f0, &f1);
-      run = 0;
-      run_items = 0;
-    }
-    const int s = (turn < chunks ? turn : turn - chunks) * kThreads + (int)threadIdx.x;
-    int32_t n = 0;
-    int64_t flat = 0;
-    bool any = false;
-    if (s < segments) {
-      const Segment g = segment(p, s);
-      flat = item_span(g) * g.items;
-      n = g.items;
-      any = !g.few && flat > 0;
-    }
-    int64_t f = flat;
-    int32_t m = n;
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t f2 = __shfl_up_sync(kAll, f, o);
-      const int32_t m2 = __shfl_up_sync(kAll, m, o);
-      if (lane >= o) f += f2, m += m2;
-    }
-    many |= __syncthreads_or(any) != 0;
-    if (lane == 31) bars->warp_flat[warp] = f, bars->warp_items[warp] = m;
-    __syncthreads();
-    int64_t before = run + f - flat;
-    int32_t before_items = run_items + m - n;
-#pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) {
-      if (k < warp) before += bars->warp_flat[k], before_items += bars->warp_items[k];
-      run += bars->warp_flat[k];
-      run_items += bars->warp_items[k];
-    }
-    if (chunks == 1) share_of(p, run, many, &f0, &f1);
-    if (s < segments) {
-      // Every CTA needs its prefixes' first items for its slots: all write the
-      // same values.
-      if (s < b.groups) items[s] = before_items;
-      if (blockIdx.x == 0 && turn < chunks) {
-        const int len = s < b.groups ? b.prefix_lens[s] : b.lens[s - b.groups];
-        if (len > (s < b.groups ? far_len(p, s) : own_len(p, s - b.groups)) && len > 0)
-          atomicOr(p.cache.err, kErrRange);
-      }
-      if (before <= f0 && f0 < before + flat) bars->seg = s, bars->start = before;
-    }
-  }
-  __syncthreads();
-  Walk walk;
-  walk.s = 0;
-  walk.start = walk.from = walk.to = 0;
-  walk.tile = -1;
-  if (f0 >= f1) return walk;
-  walk.s = bars->seg;
-  walk.start = bars->start;
-  walk.from = f0;
-  walk.to = f1;
-  return walk;
-}
-
 template <int DIM>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ AttentionParams p,
@@ -1131,13 +1179,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   wait_prerequisites();
-  const Walk walk = share_out(p, bars);
   const Ctl ctl{p.cache.err, p.wait_limit ? p.wait_limit : kDefaultWaitLimit, &bars->abort};
   if (warp < 8) {
     softmax_team<DIM>(p, smem, bars, ctl, (uint32_t)(warp >> 2));
   } else if (warp == kProducerWarp) {
-    produce_kv<DIM>(p, maps.map, smem, bars, walk, ctl);
+    produce_kv<DIM>(p, maps.map, smem, bars, ctl);
   } else {
+    if (blockIdx.x == gridDim.x - 1) note_segments(p);
     issue_products<DIM>(p, smem, bars, ctl);
   }
   __syncwarp();
@@ -1201,15 +1249,14 @@ __global__ void __launch_bounds__(kJoinThreads)
   const BatchView& b = p.batch;
   const int token = (int)blockIdx.x, head = (int)blockIdx.y;
   const int seq = b.chunk == 1 ? token : token / b.chunk, i = token - seq * b.chunk;
-  const int gq = p.heads / p.kv_heads, kvh = head / gq, h = head - kvh * gq;
-  const int in_seq = i * gq + h, seq_rows = b.chunk * gq;
+  const int kvh = head / p.gq, h = head - kvh * p.gq, in_seq = i * p.gq + h;
   wait_prerequisites();
   Side far, own;
   far.n = own.n = 0;
   const int fresh = fresh_of(b, seq);
   if (i < fresh) {
     if (own_len(p, seq) > 0)
-      own = side_of(p, false, seq_rows, in_seq, kvh, (int64_t)seq * p.ws.own_items);
+      own = side_of(p, false, p.seq_rows, in_seq, kvh, (int64_t)seq * p.ws.own_items);
     for (int g0 = 0; g0 < b.groups; g0 += 32) {
       const int g = g0 + lane;
       int first = 0, end = 0, len = 0, item = 0;
@@ -1226,8 +1273,8 @@ __global__ void __launch_bounds__(kJoinThreads)
         end = min(__shfl_sync(kAll, end, from), b.sequences);
         item = __shfl_sync(kAll, item, from);
         if (__shfl_sync(kAll, len, from) > 0)
-          far = side_of(p, true, (end - first) * seq_rows, (seq - first) * seq_rows + in_seq, kvh,
-                        item);
+          far = side_of(p, true, (end - first) * p.seq_rows, (seq - first) * p.seq_rows + in_seq,
+                        kvh, item);
         break;
       }
     }

@@ -74,7 +74,8 @@ cudaError_t launch_rope(const RopeParams& p, int in_type, int out_type, int sm_c
 // heads, tiles), which the CTAs share out equally.  What a CTA does of an item is
 // a part; each of its two softmax teams leaves the part's running maximum, sum
 // and weighted values in the workspace, and a second kernel joins them.
-constexpr int kKvTile = 128;
+constexpr int kKvShift = 7;
+constexpr int kKvTile = 1 << kKvShift;
 constexpr int kTeamRows = 128;
 constexpr int kPairRows = 2 * kTeamRows;
 constexpr int kFewRows = 16;  // rows of a segment that are multiplied without TMEM
@@ -112,7 +113,9 @@ struct AttentionParams {
   uint8_t* workspace;
   AttentionWorkspace ws;
   int32_t ctas;
+  int32_t gq, seq_rows;       // heads / kv_heads; rows of a sequence for a key head
   int32_t few_heads, few_tokens;  // of a tile of a segment of few rows
+  int32_t few_shift, few_items;   // log2 of its tokens; kv_heads / few_heads
   uint32_t wait_limit;        // polls before a bounded wait gives up (0: default)
 };
 // The pages of K and V as [pages][kv_heads][page_size][dim], 128-byte swizzle: with

@@ -13,6 +13,7 @@ namespace {
 
 constexpr int32_t kMaxTokens = 1 << 24;
 constexpr int32_t kMaxHeads = 1 << 12;
+constexpr int64_t kMaxRows = 1 << 30;  // of attention: tokens x query heads of a key head
 constexpr int32_t kMaxDim = 256;
 constexpr int32_t kMaxPageSize = 1 << 20;
 constexpr int64_t kMaxStride = 1ll << 39;  // elements: products with 2^24 stay in 64 bits
@@ -147,7 +148,8 @@ bool page_map(const nwc_kv_cache& c, uint16_t* base, int64_t page_stride, int64_
 
 bool attention_shape(const nwc_kv_cache* c, const nwc_kv_batch* b, int32_t heads) {
   return good_cache(c) && good_batch(b) && heads >= 1 && heads <= kMaxHeads &&
-         heads % c->kv_heads == 0;
+         heads % c->kv_heads == 0 &&
+         (int64_t)b->sequences * b->new_tokens * (heads / c->kv_heads) <= kMaxRows;
 }
 
 }  // namespace
@@ -244,6 +246,10 @@ nwc_status nwc_kv_attention(const nwc_kv_cache* cache, const nwc_kv_batch* batch
   p.wait_limit = nwc::wait_limit();
   p.few_heads = nwc::few_heads_of(cache->kv_heads);
   p.few_tokens = nwc::kKvTile / p.few_heads;
+  for (p.few_shift = 0; (1 << p.few_shift) < p.few_tokens;) ++p.few_shift;
+  p.few_items = cache->kv_heads / p.few_heads;
+  p.gq = heads / cache->kv_heads;
+  p.seq_rows = batch->new_tokens * p.gq;
   nwc::PageMaps maps;
   for (int i = 0; i < 4; ++i) {
     const int tokens = i < 2 ? nwc::kKvTile : p.few_tokens, per = i < 2 ? 1 : p.few_heads;

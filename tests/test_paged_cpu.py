@@ -128,6 +128,7 @@ def test_attention_arguments(lib):
                dict(heads=0), dict(heads=12), dict(scale=math.nan), dict(scale=math.inf),
                dict(lse=2)):
         assert status(**kw) == INVALID, kw
+    assert status(c=cache(lib, kv_heads=1), b=batch(lib, sequences=1 << 20), heads=2048) == INVALID
     for dim in (8, 96, 256):
         assert status(c=cache(lib, dim=dim)) == 2      # NWC_ERR_UNSUPPORTED
     n = ctypes.c_uint64()
