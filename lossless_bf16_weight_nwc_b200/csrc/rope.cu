@@ -7,10 +7,13 @@
 // on the store.  The angle is reduced to turns in 64 bits: at position 10^6 an
 // FP32 product would already be off by 0.06 rad.
 //
-// A head takes dim / 8 lanes (padded to 8, 16 or 32), each holding the two
-// quads of elements that rotate into each other, so that the rotation needs no
-// exchange and the norm one butterfly; a warp holds 32 / G heads times U, all of
-// one token and one kind (q, k or v), and evaluates the angles once for them.
+// A head takes dim / 8 lanes (padded to 8, 16 or 32), each holding the two quads of
+// elements that rotate into each other, so that the rotation needs no exchange and
+// the norm one butterfly.  A block takes a few tokens: it works out their places and
+// each angle once, into shared memory, then its warps run over the tokens' heads,
+// loading the next while they turn the last.  What bounds it is memory for a prompt
+// and the chain of loads for a few tokens, which get a block for every four warps'
+// heads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,25 +28,60 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kRopeWarps = 4;
+constexpr int kMaxDim = 256;
 
-__device__ __forceinline__ void load4(const float* p, bool vec, float (&v)[4]) {
+// Four elements as they lie in memory, and as FP32.
+struct Raw32 {
+  float v[4];
+};
+struct Raw16 {
+  uint32_t v[2];
+};
+template <typename T>
+struct RawOf {
+  using type = Raw32;
+};
+template <>
+struct RawOf<__nv_bfloat16> {
+  using type = Raw16;
+};
+__device__ __forceinline__ Raw32 load_raw(const float* p, bool vec) {
+  Raw32 r;
   if (vec) {
     const float4 f = *reinterpret_cast<const float4*>(p);
-    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    r.v[0] = f.x, r.v[1] = f.y, r.v[2] = f.z, r.v[3] = f.w;
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = p[i];
+    for (int i = 0; i < 4; ++i) r.v[i] = p[i];
   }
+  return r;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, bool vec, float (&v)[4]) {
+__device__ __forceinline__ Raw16 load_raw(const __nv_bfloat16* p, bool vec) {
+  Raw16 r;
   if (vec) {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+    r.v[0] = u.x, r.v[1] = u.y;
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __bfloat162float(p[i]);
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    r.v[0] = h[0] | (uint32_t)h[1] << 16;
+    r.v[1] = h[2] | (uint32_t)h[3] << 16;
   }
+  return r;
+}
+__device__ __forceinline__ void widen(const Raw32& r, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = r.v[i];
+}
+__device__ __forceinline__ void widen(const Raw16& r, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[2 * i] = __uint_as_float(r.v[i] << 16);
+    v[2 * i + 1] = __uint_as_float(r.v[i] & 0xFFFF0000u);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, bool vec, float (&v)[4]) {
+  widen(load_raw(p, vec), v);
 }
 __device__ __forceinline__ void store4(float* p, bool vec, const float (&v)[4]) {
   if (vec) {
@@ -64,21 +102,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, bool vec, const float (
     for (int i = 0; i < 4; ++i) p[i] = __float2bfloat16_rn(v[i]);
   }
 }
-__device__ __forceinline__ void load_weights(const void* w, bool f32, int oa, int ob,
-                                             float (&wa)[4], float (&wb)[4]) {
-  if (f32) {
-    load4(static_cast<const float*>(w) + oa, false, wa);
-    load4(static_cast<const float*>(w) + ob, false, wb);
-  } else {
-    load4(static_cast<const __nv_bfloat16*>(w) + oa, false, wa);
-    load4(static_cast<const __nv_bfloat16*>(w) + ob, false, wb);
-  }
-}
-
-struct Quads {
-  float a[4], b[4];
-};
-
 // Row `row` of the batch as a token of its sequence.
 struct Place {
   bool real;         // a new token (not padding)
@@ -118,137 +141,247 @@ __device__ __forceinline__ Place place_of(const CacheView& c, const BatchView& b
   return at;
 }
 
-// G lanes a head, U heads a group of lanes; vec_in, vec_out: quads are aligned
-// for whole loads and stores.
-template <typename TIn, typename TOut, int G, int U>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(
-    const __grid_constant__ RopeParams p, bool vec_in, bool vec_out, int jobs_q, int jobs_k,
-    int jobs) {
-  allow_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  const int64_t token64 = w / jobs;
-  const int job = (int)(w - token64 * jobs);
-  if (token64 >= p.tokens) return;
-  const int token = (int)token64;
-  const int kind = job < jobs_q ? 0 : job < jobs_q + jobs_k ? 1 : 2;
-  constexpr int kHeads = 32 / G;
-  const int head0 = (kind == 0 ? job : kind == 1 ? job - jobs_q : job - jobs_q - jobs_k) *
-                        (kHeads * U) + lane / G;
-  const int heads = kind == 0 ? p.heads : p.kv_heads;
-  const int u = lane % G;
-  const bool on = u * 8 < p.dim;
-  // The two quads of this lane, and whether they rotate.
-  const int half = p.rotary / 2;
-  const bool rot = kind < 2 && on && u * 8 < p.rotary;
-  const int oa = rot && !p.interleaved ? 4 * u : 8 * u;
-  const int ob = rot && !p.interleaved ? half + 4 * u : 8 * u + 4;
-  wait_prerequisites();
+constexpr int kMaxTokens = 4;   // of a block
+constexpr int kBlocks = 5;      // an SM, for prompts: what registers leave without spills
 
-  Place at;
-  at.real = true;
-  at.slot_page = -1;
-  at.slot = 0;
-  if (p.append) {
-    at = place_of(p.cache, p.batch, token, lane);
-  } else {
-    at.position = p.positions_64 ? static_cast<const int64_t*>(p.positions)[token]
-                                 : (int64_t)static_cast<const int32_t*>(p.positions)[token];
+// What a warp does with one kind of a token's heads.
+struct Turn {
+  bool real;                // else zeros are stored
+  bool norm, rotate, interleaved;
+  float inv_dim, eps;
+  float c[4], s[4];         // of the lane's pairs
+  float wa[4], wb[4];       // weights of its quads
+};
+
+// The raw quads of U groups of heads (32 / G heads each): first, first + step, ...
+template <typename TIn, int U>
+struct Batch {
+  typename RawOf<TIn>::type q[U][2];
+};
+template <typename TIn, int G, bool VEC>
+__device__ __forceinline__ void load_group(typename RawOf<TIn>::type (&q)[2], const TIn* src,
+                                           int64_t src_group, int quad, bool on, int g,
+                                           int heads) {
+  if (on && g * (32 / G) + (int)(threadIdx.x & 31) / G < heads) {
+    q[0] = load_raw(src + g * src_group, VEC);
+    q[1] = load_raw(src + g * src_group + quad, VEC);
   }
-  const bool to_cache = p.append && kind > 0;
-  if (to_cache && at.slot_page < 0) return;
+}
 
-  const HeadsView& in = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-  const TIn* src = static_cast<const TIn*>(in.data) + (int64_t)token * in.token_stride;
-  Quads x[U];
+// Heads in groups of this warp, U at a time.  src and dst are the lane's first quads
+// in group 0, the second ones `quad` elements on.  The first U groups are in `raw`;
+// where `next` is given, those of the next token replace them as they are used.
+template <typename TIn, typename TOut, int G, int U, bool VEC_IN, bool VEC_OUT>
+__device__ __forceinline__ void turn_heads(const Turn& k, Batch<TIn, U>& raw, const TIn* src,
+                                           int64_t src_group, const TIn* next, TOut* dst,
+                                           int64_t dst_group, int quad, bool on, int first,
+                                           int step, int groups, int heads,
+                                           bool place = true) {
+  const int in_group = (int)(threadIdx.x & 31) / G;
+#pragma unroll 1
+  for (int g0 = first; g0 < groups; g0 += U * step) {
+    if (g0 != first) {
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    const int h = head0 + k * kHeads;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[k].a[i] = x[k].b[i] = 0.f;
-    if (on && at.real && h < heads) {
-      load4(src + (int64_t)h * in.head_stride + oa, vec_in, x[k].a);
-      load4(src + (int64_t)h * in.head_stride + ob, vec_in, x[k].b);
+      for (int j = 0; j < U; ++j)
+        load_group<TIn, G, VEC_IN>(raw.q[j], src, src_group, quad, on, g0 + j * step, heads);
     }
-  }
-  if (at.real) {
-    float c[4], s[4];
-    if (rot) {
+    const bool last = g0 + U * step >= groups;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // Pair i of the lane: (a_i, b_i), or neighbours when interleaved.
-        const double turns =
-            (double)at.position * p.freq[4 * u + i] * 0.15915494309189533577;  // 1 / (2 pi)
-        sincospif(2.f * (float)(turns - rint(turns)), &s[i], &c[i]);
+    for (int j = 0; j < U; ++j) {
+      float a[4], b[4];
+      widen(raw.q[j][0], a);
+      widen(raw.q[j][1], b);
+      if (!k.real) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = b[i] = 0.f;
       }
-    }
-    const void* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-    if (weight) {
-      float wa[4] = {}, wb[4] = {};
-      if (on) load_weights(weight, p.weight_f32 != 0, oa, ob, wa, wb);
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
+      if (next && last)
+        load_group<TIn, G, VEC_IN>(raw.q[j], next, src_group, quad, on, first + j * step, heads);
+      if (k.norm) {
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum += x[k].a[i] * x[k].a[i] + x[k].b[i] * x[k].b[i];
+        for (int i = 0; i < 4; ++i) sum += a[i] * a[i] + b[i] * b[i];
 #pragma unroll
         for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        const float r = rsqrtf(sum / (float)p.dim + p.eps);
+        const float r = rsqrtf(sum * k.inv_dim + k.eps);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[k].a[i] *= r * wa[i];
-          x[k].b[i] *= r * wb[i];
-        }
+        for (int i = 0; i < 4; ++i) a[i] *= r * k.wa[i], b[i] *= r * k.wb[i];
       }
-    }
-    if (rot) {
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        float* a = x[k].a;
-        float* b = x[k].b;
-        if (p.interleaved) {
+      if (k.rotate) {
+        if (k.interleaved) {
           // The lane's eight elements are pairs 4u .. 4u + 3 in order.
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float& e = i < 2 ? a[2 * i] : b[2 * i - 4];
             float& o = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
             const float e0 = e, o0 = o;
-            e = e0 * c[i] - o0 * s[i];
-            o = o0 * c[i] + e0 * s[i];
+            e = e0 * k.c[i] - o0 * k.s[i];
+            o = o0 * k.c[i] + e0 * k.s[i];
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float a0 = a[i], b0 = b[i];
-            a[i] = a0 * c[i] - b0 * s[i];
-            b[i] = b0 * c[i] + a0 * s[i];
+            a[i] = a0 * k.c[i] - b0 * k.s[i];
+            b[i] = b0 * k.c[i] + a0 * k.s[i];
           }
         }
       }
+      const int g = g0 + j * step;
+      if (place && on && g * (32 / G) + in_group < heads) {
+        store4(dst + g * dst_group, VEC_OUT, a);
+        store4(dst + g * dst_group + quad, VEC_OUT, b);
+      }
     }
   }
-  if (!on) return;
+}
+
+// G lanes a head; VEC: all quads are aligned for whole loads and stores.  Blocks are
+// token blocks x `splits`, the latter sharing a token's heads.
+template <typename TIn, typename TOut, int G, int U, bool VEC>
+__global__ void __launch_bounds__(kRopeWarps * 32, U == 4 ? kBlocks : 1) rope_kernel(
+    const __grid_constant__ RopeParams p, int block_tokens, int splits, int groups_q,
+    int groups_k) {
+  __shared__ float2 turn[kMaxTokens][kMaxDim / 2];   // cosine and sine of each pair
+  __shared__ Place places[kMaxTokens];
+  allow_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int split = (int)(blockIdx.x % (unsigned)splits);
+  const int token0 = (int)(blockIdx.x / (unsigned)splits) * block_tokens;
+  const int tokens = min(block_tokens, p.tokens - token0);
+  constexpr int kHeads = 32 / G;
+  const int u = lane % G, in_group = lane / G;
+  const bool on = u * 8 < p.dim;
+  // The two quads of this lane, in a head that rotates; else 8 u and the next.
+  const int half = p.rotary / 2;
+  Turn k;
+  k.rotate = u * 8 < p.rotary;
+  k.interleaved = p.interleaved != 0;
+  k.inv_dim = 1.f / (float)p.dim;
+  k.eps = p.eps;
+  const bool apart = k.rotate && !k.interleaved;
+  const int oa = apart ? 4 * u : 8 * u, quad = apart ? half : 4;
+  const int first = split * kRopeWarps + warp, step = splits * kRopeWarps;
+  // Few k and v heads: of the warps behind the last with q, and with k, first.
+  const int first_k = (first + step - groups_q % step) % step;
+  const int first_v = (first_k + step - groups_k % step) % step;
+  const int64_t q_group = kHeads * p.q.head_stride, k_group = kHeads * p.k.head_stride,
+                v_group = kHeads * p.v.head_stride;
+  const TIn* q_src = static_cast<const TIn*>(p.q.data) + (int64_t)token0 * p.q.token_stride +
+                     in_group * p.q.head_stride + oa;
+  const TIn* k_src = static_cast<const TIn*>(p.k.data) + (int64_t)token0 * p.k.token_stride +
+                     in_group * p.k.head_stride + oa;
+  const TIn* v_src = static_cast<const TIn*>(p.v.data) + (int64_t)token0 * p.v.token_stride +
+                     in_group * p.v.head_stride + 8 * u;
+  wait_prerequisites();
+
+  // The first token's heads are on their way while the places and angles are found.
+  Batch<TIn, U> raw_q = {};
+  Batch<TIn, 1> raw_k = {}, raw_v = {};
+  if (p.q.data) {
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    const int h = head0 + k * kHeads;
-    if (h >= heads) continue;
-    if (to_cache) {
-      const CacheView& cv = p.cache;
-      __nv_bfloat16* d =
-          kind == 1 ? reinterpret_cast<__nv_bfloat16*>(cv.k) + at.slot_page * cv.k_page +
-                          at.slot * cv.k_token + h * cv.k_head
-                    : reinterpret_cast<__nv_bfloat16*>(cv.v) + at.slot_page * cv.v_page +
-                          at.slot * cv.v_token + h * cv.v_head;
-      // Pages are 16-byte aligned with strides of 8 elements (checked on the host).
-      store4(d + oa, true, x[k].a);
-      store4(d + ob, true, x[k].b);
+    for (int j = 0; j < U; ++j)
+      load_group<TIn, G, VEC>(raw_q.q[j], q_src, q_group, quad, on, first + j * step, p.heads);
+  }
+  if (p.k.data)
+    load_group<TIn, G, VEC>(raw_k.q[0], k_src, k_group, quad, on, first_k, p.kv_heads);
+  if (p.append)
+    load_group<TIn, G, VEC>(raw_v.q[0], v_src, v_group, 4, on, first_v, p.kv_heads);
+  for (int t = warp; t < tokens; t += kRopeWarps) {
+    Place at;
+    if (p.append) {
+      at = place_of(p.cache, p.batch, token0 + t, lane);
     } else {
-      const HeadsView& o = kind == 0 ? p.q_out : p.k_out;
-      TOut* d = static_cast<TOut*>(o.data) + (int64_t)token * o.token_stride +
-                (int64_t)h * o.head_stride;
-      store4(d + oa, vec_out, x[k].a);
-      store4(d + ob, vec_out, x[k].b);
+      at.real = true;
+      at.slot_page = at.slot = 0;
+      at.position = p.positions_64
+                        ? static_cast<const int64_t*>(p.positions)[token0 + t]
+                        : (int64_t)static_cast<const int32_t*>(p.positions)[token0 + t];
     }
+    if (lane == 0) places[t] = at;
+  }
+  float w[2][2][4];   // weights of q and of k for the lane's quads
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const void* weight = j == 0 ? p.q_weight : p.k_weight;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[j][0][i] = w[j][1][i] = 0.f;
+    if (!weight || !on) continue;
+    if (p.weight_f32) {
+      load4(static_cast<const float*>(weight) + oa, VEC, w[j][0]);
+      load4(static_cast<const float*>(weight) + oa + quad, VEC, w[j][1]);
+    } else {
+      load4(static_cast<const __nv_bfloat16*>(weight) + oa, VEC, w[j][0]);
+      load4(static_cast<const __nv_bfloat16*>(weight) + oa + quad, VEC, w[j][1]);
+    }
+  }
+  __syncthreads();
+  for (int t = 0; t < tokens; ++t) {
+    const double position = (double)places[t].position;
+    for (int i = threadIdx.x; i < half; i += kRopeWarps * 32) {
+      const double angle = position * p.freq[i] * 0.15915494309189533577;
+      float2 cs;   // the angle in turns, of which the fraction counts
+      sincospif(2.f * (float)(angle - rint(angle)), &cs.y, &cs.x);
+      turn[t][i] = cs;
+    }
+  }
+  __syncthreads();
+
+#pragma unroll 1
+  for (int t = 0; t < tokens; ++t) {
+    const Place at = places[t];
+    const int64_t token = token0 + t;
+    k.real = at.real;
+    if (k.rotate) {
+      const float4 lo = *reinterpret_cast<const float4*>(&turn[t][4 * u]);
+      const float4 hi = *reinterpret_cast<const float4*>(&turn[t][4 * u + 2]);
+      k.c[0] = lo.x, k.c[1] = lo.z, k.c[2] = hi.x, k.c[3] = hi.z;
+      k.s[0] = lo.y, k.s[1] = lo.w, k.s[2] = hi.y, k.s[3] = hi.w;
+    }
+    const bool more = t + 1 < tokens && places[t + 1].real;
+    if (p.q.data) {
+      k.norm = p.q_weight != nullptr;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k.wa[i] = w[0][0][i], k.wb[i] = w[0][1][i];
+      const TIn* src = q_src + t * p.q.token_stride;
+      turn_heads<TIn, TOut, G, U, VEC, VEC>(
+          k, raw_q, src, q_group, more ? src + p.q.token_stride : nullptr,
+          static_cast<TOut*>(p.q_out.data) + token * p.q_out.token_stride +
+              in_group * p.q_out.head_stride + oa,
+          kHeads * p.q_out.head_stride, quad, on, first, step, groups_q, p.heads);
+    }
+    if (!p.k.data) continue;
+    k.norm = p.k_weight != nullptr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k.wa[i] = w[1][0][i], k.wb[i] = w[1][1][i];
+    const TIn* src = k_src + t * p.k.token_stride;
+    const TIn* next = more ? src + p.k.token_stride : nullptr;
+    if (!p.append) {
+      turn_heads<TIn, TOut, G, 1, VEC, VEC>(
+          k, raw_k, src, k_group, next,
+          static_cast<TOut*>(p.k_out.data) + token * p.k_out.token_stride +
+              in_group * p.k_out.head_stride + oa,
+          kHeads * p.k_out.head_stride, quad, on, first_k, step, groups_k, p.kv_heads);
+      continue;
+    }
+    // Pages are 16-byte aligned with strides of 8 elements (checked on the host).  A
+    // row without a place still brings the next one's heads.
+    const CacheView& cv = p.cache;
+    const bool place = at.slot_page >= 0;
+    const int64_t page = place ? at.slot_page : 0;
+    turn_heads<TIn, __nv_bfloat16, G, 1, VEC, true>(
+        k, raw_k, src, k_group, next,
+        reinterpret_cast<__nv_bfloat16*>(cv.k) + page * cv.k_page + at.slot * cv.k_token +
+            in_group * cv.k_head + oa,
+        kHeads * cv.k_head, quad, on, first_k, step, groups_k, p.kv_heads, place);
+    Turn plain = k;
+    plain.norm = plain.rotate = false;
+    src = v_src + t * p.v.token_stride;
+    turn_heads<TIn, __nv_bfloat16, G, 1, VEC, true>(
+        plain, raw_v, src, v_group, more ? src + p.v.token_stride : nullptr,
+        reinterpret_cast<__nv_bfloat16*>(cv.v) + page * cv.v_page + at.slot * cv.v_token +
+            in_group * cv.v_head + 8 * u,
+        kHeads * cv.v_head, 4, on, first_v, step, groups_k, p.kv_heads, place);
   }
 }
 
@@ -258,13 +391,18 @@ bool quads_aligned(const HeadsView& v, int type) {
                      v.token_stride % 4 == 0 && v.head_stride % 4 == 0);
 }
 
-template <typename TIn, typename TOut, int G, int U>
-cudaError_t launch_t(const RopeParams& p, bool vi, bool vo, cudaStream_t stream) {
-  constexpr int per = 32 / G * U;
-  const int jobs_q = p.q.data ? (p.heads + per - 1) / per : 0;
-  const int jobs_k = p.k.data ? (p.kv_heads + per - 1) / per : 0;
-  const int jobs = jobs_q + jobs_k * (p.append ? 2 : 1);
-  const int64_t blocks = ((int64_t)p.tokens * jobs + kRopeWarps - 1) / kRopeWarps;
+template <typename TIn, typename TOut, int G, bool VEC>
+cudaError_t launch_t(const RopeParams& p, int sm_count, cudaStream_t stream) {
+  constexpr int kHeads = 32 / G;
+  const int groups_q = p.q.data ? (p.heads + kHeads - 1) / kHeads : 0;
+  const int groups_k = p.k.data ? (p.kv_heads + kHeads - 1) / kHeads : 0;
+  const int groups = groups_q + groups_k * (p.append ? 2 : 1);
+  // Four tokens a block share the work on angles; until such blocks fill the device
+  // a token each, its heads over as many blocks as it takes for a head group a warp.
+  const bool large = p.tokens >= sm_count * 2 * kMaxTokens;
+  const int block_tokens = large ? kMaxTokens : 1;
+  const int splits = large ? 1 : (groups + kRopeWarps - 1) / kRopeWarps;
+  const int64_t blocks = ((int64_t)p.tokens + block_tokens - 1) / block_tokens * splits;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
@@ -275,42 +413,41 @@ cudaError_t launch_t(const RopeParams& p, bool vi, bool vo, cudaStream_t stream)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_kernel<TIn, TOut, G, U>, p, vi, vo, jobs_q, jobs_k,
-                            jobs);
+  // Four head groups of q in flight a warp where it has as many.
+  return large ? cudaLaunchKernelEx(&cfg, rope_kernel<TIn, TOut, G, 4, VEC>, p, block_tokens,
+                                    splits, groups_q, groups_k)
+               : cudaLaunchKernelEx(&cfg, rope_kernel<TIn, TOut, G, 1, VEC>, p, block_tokens,
+                                    splits, groups_q, groups_k);
 }
 
-template <typename TIn, typename TOut, int G>
-cudaError_t launch_u(const RopeParams& p, bool vi, bool vo, int sm_count,
-                     cudaStream_t stream) {
-  // One head a lane group until that fills the device with warps twice over;
-  // then four, which share their angles and keep four times the loads in flight.
-  const int64_t warps =
-      ((int64_t)p.tokens * (p.heads + 2 * p.kv_heads) * G + 31) / 32;
-  if (warps < (int64_t)sm_count * 128) return launch_t<TIn, TOut, G, 1>(p, vi, vo, stream);
-  return launch_t<TIn, TOut, G, 4>(p, vi, vo, stream);
+template <typename TIn, typename TOut, bool VEC>
+cudaError_t launch_g(const RopeParams& p, int sm_count, cudaStream_t stream) {
+  if (p.dim <= 64) return launch_t<TIn, TOut, 8, VEC>(p, sm_count, stream);
+  if (p.dim <= 128) return launch_t<TIn, TOut, 16, VEC>(p, sm_count, stream);
+  return launch_t<TIn, TOut, 32, VEC>(p, sm_count, stream);
 }
 
 template <typename TIn, typename TOut>
-cudaError_t launch_g(const RopeParams& p, bool vi, bool vo, int sm_count,
-                     cudaStream_t stream) {
-  if (p.dim <= 64) return launch_u<TIn, TOut, 8>(p, vi, vo, sm_count, stream);
-  if (p.dim <= 128) return launch_u<TIn, TOut, 16>(p, vi, vo, sm_count, stream);
-  return launch_u<TIn, TOut, 32>(p, vi, vo, sm_count, stream);
+cudaError_t launch_v(const RopeParams& p, bool vec, int sm_count, cudaStream_t stream) {
+  return vec ? launch_g<TIn, TOut, true>(p, sm_count, stream)
+             : launch_g<TIn, TOut, false>(p, sm_count, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeParams& p, int in_type, int out_type, int sm_count,
                         cudaStream_t stream) {
-  const bool vi = quads_aligned(p.q, in_type) && quads_aligned(p.k, in_type) &&
-                  quads_aligned(p.v, in_type);
-  const bool vo = quads_aligned(p.q_out, out_type) && quads_aligned(p.k_out, out_type);
+  const uintptr_t unit = p.weight_f32 ? 16 : 8;
+  const bool vec = quads_aligned(p.q, in_type) && quads_aligned(p.k, in_type) &&
+                   quads_aligned(p.v, in_type) && quads_aligned(p.q_out, out_type) &&
+                   quads_aligned(p.k_out, out_type) &&
+                   (reinterpret_cast<uintptr_t>(p.q_weight) % unit) == 0 &&
+                   (reinterpret_cast<uintptr_t>(p.k_weight) % unit) == 0;
   if (in_type == kTypeF32)
-    return out_type == kTypeF32 ? launch_g<float, float>(p, vi, vo, sm_count, stream)
-                                : launch_g<float, __nv_bfloat16>(p, vi, vo, sm_count, stream);
-  return out_type == kTypeF32
-             ? launch_g<__nv_bfloat16, float>(p, vi, vo, sm_count, stream)
-             : launch_g<__nv_bfloat16, __nv_bfloat16>(p, vi, vo, sm_count, stream);
+    return out_type == kTypeF32 ? launch_v<float, float>(p, vec, sm_count, stream)
+                                : launch_v<float, __nv_bfloat16>(p, vec, sm_count, stream);
+  return out_type == kTypeF32 ? launch_v<__nv_bfloat16, float>(p, vec, sm_count, stream)
+                              : launch_v<__nv_bfloat16, __nv_bfloat16>(p, vec, sm_count, stream);
 }
 
 }  // namespace nwc

@@ -24,6 +24,8 @@ import torch
 
 from . import _lib
 
+# The C calls themselves: _lib's wrappers also take tensors, which costs a call 1 us.
+_LIB, _check = _lib.LIB, _lib._check
 _TYPES = {torch.bfloat16: _lib.NWC_TYPE_BF16, torch.float32: _lib.NWC_TYPE_F32}
 _HEADS = ctypes.sizeof(_lib.nwc_heads)
 _ROPE = ctypes.sizeof(_lib.nwc_rope)
@@ -86,11 +88,11 @@ def _output(t, what: str, shape, device, dtypes):
     return h
 
 
-def _new(shape, device):
-    """A new BF16 tensor [tokens, heads, dim] and its C view."""
-    t = torch.empty(shape, dtype=torch.bfloat16, device=device)
+def _new(like, shape):
+    """A new BF16 tensor of the shape of `like`, [tokens, heads, dim], and its C view."""
+    t = torch.empty_like(like, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
     dim = shape[2]
-    return t, _lib.nwc_heads(_HEADS, _lib.NWC_TYPE_BF16, t.data_ptr(), shape[1] * dim, dim)
+    return t, _lib.nwc_heads(_HEADS, 0, t.data_ptr(), shape[1] * dim, dim)
 
 
 def _vector(t, what: str, device, n: int, dtypes) -> int:
@@ -217,9 +219,9 @@ def qk_norm_rope(q, k, positions, freq=None, q_weight=None, k_weight=None, eps: 
         qo = ko = qoh = koh = None
         if out is None:
             if q is not None:
-                qo, qoh = _new((tokens, heads, dim), device)
+                qo, qoh = _new(q, (tokens, heads, dim))
             if k is not None:
-                ko, koh = _new((tokens, kv_heads, dim), device)
+                ko, koh = _new(k, (tokens, kv_heads, dim))
         else:
             qo, ko = out
             if (qo is None) != (q is None) or (ko is None) != (k is None):
@@ -231,8 +233,9 @@ def qk_norm_rope(q, k, positions, freq=None, q_weight=None, k_weight=None, eps: 
                 koh = _output(ko, "out[1]", (tokens, kv_heads, dim), device,
                               _TYPES if q is None else (qo.dtype,))
         if tokens:
-            _lib.nwc_qk_norm_rope(qh, kh, qoh, koh, tokens, heads, kv_heads, dim, at,
-                                  positions.dtype == torch.int64, rope, raw)
+            _check(_LIB.nwc_qk_norm_rope(qh, kh, qoh, koh, tokens, heads, kv_heads, dim, at,
+                                         positions.dtype == torch.int64, rope, raw),
+                   "nwc_qk_norm_rope")
     return qo, ko
 
 
@@ -391,9 +394,10 @@ class PagedKV:
             if q_out is not None:
                 qoh = _output(q_out, "q_out", shape, device, _BF16)
             elif q is not None:
-                q_out, qoh = _new(shape, device)
+                q_out, qoh = _new(q, shape)
             if rows:
-                _lib.nwc_kv_append(self._view, view, qh, qoh, heads, kh, vh, rope, raw)
+                _check(_LIB.nwc_kv_append(self._view, view, qh, qoh, heads, kh, vh, rope, raw),
+                       "nwc_kv_append")
         return q_out
 
     def attend(self, batch: PagedBatch, q, scale: float | None = None, out=None,
@@ -418,7 +422,7 @@ class PagedKV:
             scale = self.dim ** -0.5
         with _on(self.device, stream) as raw:
             if out is None:
-                out, oh = _new(shape, self.device)
+                out, oh = _new(q, shape)
             else:
                 oh = _output(out, "out", shape, self.device, _BF16)
             lse = torch.empty((rows, heads), dtype=torch.float32,
@@ -432,7 +436,9 @@ class PagedKV:
                 # From torch's allocator on the call's stream: calls on different
                 # streams, and captured graphs, each have their own.
                 ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-                _lib.nwc_kv_attention(self._view, view, qh, heads, scale, oh, lse, ws, need, raw)
+                _check(_LIB.nwc_kv_attention(self._view, view, qh, heads, scale, oh,
+                                             None if lse is None else lse.data_ptr(),
+                                             ws.data_ptr(), need, raw), "nwc_kv_attention")
         return (out, lse) if return_lse else out
 
 
