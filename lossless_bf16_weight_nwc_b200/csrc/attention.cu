@@ -117,50 +117,63 @@ struct Segment {
 
 // What a tile costs by the kind of its segment, and what each item adds at its start
 // (a part's end and the next one's beginning), in units of about 400 cycles: fitted
-// to the times of CTAs with different parts (heads of 64, then of 128).
-__device__ constexpr int kCost[2][3] = {{3, 6, 9}, {4, 9, 10}};
-__device__ constexpr int kLead[2][3] = {{8, 7, 14}, {9, 8, 33}};
+// to the times of CTAs with different parts.  (Selects: a table would be a load.)
 constexpr int kCostMost = 10;
+__device__ __forceinline__ int cost_of(Kind kind, bool wide) {
+  return kind == kFew ? (wide ? 4 : 3) : kind == kOne ? (wide ? 9 : 6) : (wide ? 10 : 9);
+}
+__device__ __forceinline__ int lead_of(Kind kind, bool wide) {
+  return kind == kFew ? (wide ? 9 : 8) : kind == kOne ? (wide ? 8 : 7) : (wide ? 33 : 14);
+}
 
 __device__ __forceinline__ int fresh_of(const BatchView& b, int seq) {
   return b.q_lens ? min(max(b.q_lens[seq], 0), b.chunk) : b.chunk;
 }
-__device__ __forceinline__ int own_len(const AttentionParams& p, int seq) {
-  const int64_t cap = min((int64_t)p.batch.table_width << p.cache.page_shift, kMaxTokens);
-  return (int)min((int64_t)max(p.batch.lens[seq], 0), cap);
+__device__ __forceinline__ int capped(const AttentionParams& p, int len, int width) {
+  const int64_t cap = min((int64_t)width << p.cache.page_shift, kMaxTokens);
+  return (int)min((int64_t)max(len, 0), cap);
 }
-__device__ __forceinline__ int far_len(const AttentionParams& p, int g) {
-  const int64_t cap = min((int64_t)p.batch.prefix_width << p.cache.page_shift, kMaxTokens);
-  return (int)min((int64_t)max(p.batch.prefix_lens[g], 0), cap);
+
+// What the tables say of segment s.
+struct Raw {
+  int len, first, end;   // first sequence of a prefix and the one behind its last; or
+                         // 0 and the sequence's new tokens
+};
+__device__ __forceinline__ Raw raw_segment(const BatchView& b, int s, bool in) {
+  const bool far = s < b.groups;
+  const int seq = far ? 0 : s - b.groups;
+  Raw r;
+  r.len = r.first = 0;
+  r.end = 1;
+  if (in) r.len = *(far ? b.prefix_lens + s : b.lens + seq);
+  if (in && far) r.first = b.group_start[s];
+  if (in && (far || b.q_lens)) r.end = *(far ? b.group_start + s + 1 : b.q_lens + seq);
+  return r;
 }
 // cap: the most that an item's lead may cost; negative: every tile costs 1 and a
-// lead nothing.  (No divisions here: a part's announcement is on the way to its first
-// byte.)
-__device__ __forceinline__ Segment segment(const AttentionParams& p, int s, int cap) {
+// lead nothing.  (No divisions or branches here: a part's announcement is on the way
+// to its first byte.)
+__device__ __forceinline__ void price(const AttentionParams& p, Segment& g, int cap) {
+  g.cost = cap < 0 ? 1 : cost_of(g.kind, p.dim == 128);
+  g.lead = cap < 0 ? 0 : min(lead_of(g.kind, p.dim == 128), cap);
+}
+__device__ __forceinline__ Segment segment_of(const AttentionParams& p, int s, const Raw& raw) {
   const BatchView& b = p.batch;
   Segment r;
-  if (s < b.groups) {
-    r.far = true;
-    r.seq0 = min(max(b.group_start[s], 0), b.sequences);
-    const int end = min(max(b.group_start[s + 1], r.seq0), b.sequences);
-    r.rows = (end - r.seq0) * p.seq_rows;
-    r.len = far_len(p, s);
-    if (r.rows == 0) r.len = 0;
-  } else {
-    r.far = false;
-    r.seq0 = s - b.groups;
-    r.rows = p.seq_rows;
-    r.len = own_len(p, r.seq0);
-    if (b.q_lens && b.q_lens[r.seq0] <= 0) r.len = 0;
-  }
+  r.far = s < b.groups;
+  const int first = min(max(raw.first, 0), b.sequences);
+  const int end = min(max(raw.end, first), b.sequences);
+  r.seq0 = r.far ? first : s - b.groups;
+  r.rows = r.far ? (end - first) * p.seq_rows : p.seq_rows;
+  r.len = capped(p, raw.len, r.far ? b.prefix_width : b.table_width);
+  if (r.far ? r.rows == 0 : raw.end <= 0) r.len = 0;
   r.few = r.rows <= kFewRows;
+  r.kind = r.few ? kFew : r.rows <= kTeamRows ? kOne : kBoth;
   const int shift = r.few ? p.few_shift : kKvShift;
   r.tiles = (int)(((uint32_t)r.len + (1u << shift) - 1) >> shift);
   r.items = r.few ? (r.rows > 0 ? p.few_items : 0)
                   : (r.rows + kPairRows - 1) / kPairRows * p.kv_heads;
-  r.kind = r.few ? kFew : r.rows <= kTeamRows ? kOne : kBoth;
-  r.cost = cap < 0 ? 1 : kCost[p.dim == 128][r.kind];
-  r.lead = cap < 0 ? 0 : min(kLead[p.dim == 128][r.kind], cap);
+  r.cost = r.lead = 0;
   return r;
 }
 // The tiles lie on an axis of costs; of the CTAs that share it, c has those that start in
@@ -183,56 +196,69 @@ __device__ __forceinline__ int32_t* spans_of(const AttentionParams& p, int s, in
 __device__ __forceinline__ int64_t item_span(const Segment& g) {
   return g.tiles ? g.lead + (int64_t)g.tiles * g.cost : 0;
 }
-// The first tile of the segment (counted over its items) that starts at or behind
-// `at` (>= 0) of its part of the axis.
-__device__ __forceinline__ int64_t tile_from(const Segment& g, int64_t at) {
+// The first tile that starts at or behind `at` (>= 0) of its part of the axis: item and
+// tile of the item.
+struct At {
+  int item, tile;
+};
+__device__ __forceinline__ At tile_from(const Segment& g, int64_t at) {
   const int64_t span = item_span(g), item = divide(at, span), in = at - item * span - g.lead;
-  return item * g.tiles + (in > 0 ? divide(in + g.cost - 1, g.cost) : 0);
+  At r;
+  r.item = (int)item;
+  r.tile = in > 0 ? (int)divide(in + g.cost - 1, g.cost) : 0;
+  return r;   // r.tile may be g.tiles: the item has none behind `at`
 }
 
 // The parts of a CTA in order: those of the tiles that start in [from, to) of the
-// axis, from segment s, which starts at `start`; `tile`, the first one left of it.
+// axis, from segment s, which starts at `start`.
 struct Walk {
   int s, cap;
-  int64_t start, from, to, tile;
-  int64_t item0;   // the segment's first item, counted over the prefixes' or the own
+  int64_t start, from, to;
+  int64_t item0;     // the segment's first item, counted over the prefixes' or the own
+  bool open;         // the segment has been looked up
+  Segment g;
+  At at, end;        // its tiles left
   __device__ __forceinline__ bool next(const AttentionParams& p, Part& part) {
     const int segments = p.batch.groups + p.batch.sequences;
-    while (s < segments && start < to) {
-      const Segment g = segment(p, s, cap);
-      const int64_t span = item_span(g) * g.items;
-      if (tile < 0 && span > 0) tile = from > start ? tile_from(g, from - start) : 0;
-      const int64_t end =
-          to - start >= span ? (int64_t)g.tiles * g.items : tile_from(g, to - start);
-      if (tile >= end || span == 0) {
+    for (;;) {
+      if (!open) {
+        if (s >= segments || start >= to) return false;
+        g = segment_of(p, s, raw_segment(p.batch, s, true));
+        price(p, g, cap);
+        at.item = at.tile = 0;
+        end.item = g.tiles ? g.items : 0;
+        end.tile = 0;
+        const int64_t span = item_span(g) * g.items;
+        if (span > 0 && from > start) at = tile_from(g, from - start);
+        if (span > 0 && to - start < span) end = tile_from(g, to - start);
         start += span;
-        tile = -1;
-        item0 = ++s == p.batch.groups ? 0 : item0 + g.items;
-        continue;
+        open = true;
       }
-      const int item = (int)divide(tile, g.tiles);
-      part.tile0 = (int)(tile - (int64_t)item * g.tiles);
-      part.n = (int)min((int64_t)(g.tiles - part.tile0), end - tile);
-      const int block = g.few ? 0 : item / p.kv_heads;
-      part.kvh = g.few ? item * p.few_heads : item - block * p.kv_heads;
-      part.base = block * kPairRows;
-      part.rows = min(g.rows - part.base, kPairRows);
-      part.kind = g.few ? kFew : part.rows <= kTeamRows ? kOne : kBoth;
-      part.far = g.far;
-      part.seq0 = g.seq0;
-      part.len = g.len;
-      // The slot of its results: item + CTA is different for any two parts, as each
-      // next part has a later item, a later CTA or both.
-      const int64_t slot = item0 + item + blockIdx.x;
-      const bool room = slot < (g.far ? p.ws.far_slots : p.ws.own_slots);
-      part.place = room ? slot * (g.far ? kPairRows : p.ws.own_rows) : -1;
-      part.spans = spans_of(p, s, item0 + item);
-      part.first = part.tile0 == 0;
-      part.last = part.tile0 + part.n == g.tiles;
-      tile += part.n;
-      return true;
+      if (at.tile >= g.tiles) ++at.item, at.tile = 0;
+      if (g.tiles && (at.item < end.item || (at.item == end.item && at.tile < end.tile))) break;
+      open = false;
+      item0 = ++s == p.batch.groups ? 0 : item0 + g.items;
     }
-    return false;
+    part.tile0 = at.tile;
+    part.n = (at.item == end.item ? end.tile : g.tiles) - at.tile;
+    const int block = g.few || at.item < p.kv_heads ? 0 : at.item / p.kv_heads;
+    part.kvh = g.few ? at.item * p.few_heads : at.item - block * p.kv_heads;
+    part.base = block * kPairRows;
+    part.rows = min(g.rows - part.base, kPairRows);
+    part.kind = g.few ? kFew : part.rows <= kTeamRows ? kOne : kBoth;
+    part.far = g.far;
+    part.seq0 = g.seq0;
+    part.len = g.len;
+    // The slot of its results: item + CTA is different for any two parts, as each
+    // next part has a later item, a later CTA or both.
+    const int64_t item = item0 + at.item, slot = item + blockIdx.x;
+    const bool room = slot < (g.far ? p.ws.far_slots : p.ws.own_slots);
+    part.place = room ? slot * (g.far ? kPairRows : p.ws.own_rows) : -1;
+    part.spans = spans_of(p, s, item);
+    part.first = part.tile0 == 0;
+    part.last = part.tile0 + part.n == g.tiles;
+    at.tile += part.n;
+    return true;
   }
 };
 
@@ -280,10 +306,11 @@ __device__ __forceinline__ Row row_of(const AttentionParams& p, const Part& part
   return row;
 }
 
+// A sum over the warp of values below 2^52.
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
+  const uint32_t lo = __reduce_add_sync(kAll, (uint32_t)v & 0x3FFFFFFu);
+  const uint32_t hi = __reduce_add_sync(kAll, (uint32_t)(v >> 26));
+  return ((int64_t)hi << 26) + lo;
 }
 
 // Where this CTA's share of the axis starts: the producer warp sums the segments,
@@ -292,64 +319,67 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 // may be without a tile (the join counts on it), so a share is at least as long as
 // the widest gap between two tiles' starts, the most that a tile costs plus a lead:
 // leads are capped for it, and where that leaves none every tile costs 1.
-__device__ Walk share_out(const AttentionParams& p) {
+__device__ __forceinline__ Walk share_out(const AttentionParams& p) {
   const BatchView& b = p.batch;
   const int segments = b.groups + b.sequences;
   const int lane = threadIdx.x & 31;
   const int chunks = (segments + 127) / 128;
   Segment g[4];
-  auto take = [&](int s0, int cap) {
+  auto take = [&](int s0) {
+    Raw raw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) raw[j] = raw_segment(b, s0 + j, s0 + j < segments);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      g[j].tiles = g[j].items = 0;
-      g[j].kind = kFew;
-      if (s0 + j < segments) g[j] = segment(p, s0 + j, cap);
+      g[j] = segment_of(p, s0 + j, raw[j]);
+      if (s0 + j >= segments) g[j].tiles = g[j].items = 0;
     }
   };
-  int64_t tiles = 0, cost = 0, of_kind[3] = {0, 0, 0};   // items of each kind
+  int64_t tiles = 0, cost = 0;
+  int of_kind[3] = {0, 0, 0};   // items of each kind
 #pragma unroll 1
   for (int t = 0; t < chunks; ++t) {
-    const int s0 = t * 128 + 4 * lane;
-    take(s0, 0);
+    take(t * 128 + 4 * lane);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t all = (int64_t)g[j].tiles * g[j].items;
-      if (all == 0) continue;
       tiles += all;
-      cost += all * g[j].cost;
+      cost += all * cost_of(g[j].kind, p.dim == 128);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) of_kind[k] += g[j].kind == k ? g[j].items : 0;
+      for (int k = 0; k < 3; ++k) of_kind[k] += all > 0 && g[j].kind == k ? g[j].items : 0;
     }
   }
   tiles = warp_sum(tiles);
   cost = warp_sum(cost);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) of_kind[k] = __reduce_add_sync(kAll, of_kind[k]);
   Walk walk;
   const int64_t each = divide(cost, p.ctas) - kCostMost;
   walk.cap = each < 0 ? -1 : (int)min(each, (int64_t)1024);
   int64_t total = walk.cap < 0 ? tiles : cost;
-  if (walk.cap >= 0) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) total += warp_sum(of_kind[k]) * min(kLead[p.dim == 128][k], walk.cap);
-  }
+  for (int k = 0; k < 3; ++k)
+    total += walk.cap < 0
+                 ? 0
+                 : (int64_t)of_kind[k] * min(lead_of((Kind)k, p.dim == 128), walk.cap);
   const int ctas = (int)min((int64_t)p.ctas, max(total, (int64_t)1));
   const int c = (int)blockIdx.x;
   walk.from = c < ctas ? share(total, c, ctas) : total;
   walk.to = c < ctas ? share(total, c + 1, ctas) : total;
   walk.s = segments;
   walk.start = walk.item0 = 0;
-  walk.tile = -1;
+  walk.open = false;
   int64_t run = 0;
   int32_t run_items = 0;
 #pragma unroll 1
   for (int t = 0; t < chunks && run <= walk.from; ++t) {
     const int s0 = t * 128 + 4 * lane;
-    if (chunks > 1) take(s0, walk.cap);
+    if (chunks > 1) take(s0);
     int64_t span[4], sum = 0;
     int32_t n = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      g[j].cost = walk.cap < 0 ? 1 : kCost[p.dim == 128][g[j].kind];
-      g[j].lead = walk.cap < 0 ? 0 : min(kLead[p.dim == 128][g[j].kind], walk.cap);
+      price(p, g[j], walk.cap);
       span[j] = item_span(g[j]) * g[j].items;
       sum += span[j];
       n += g[j].items;
@@ -367,7 +397,8 @@ __device__ Walk share_out(const AttentionParams& p) {
     at += run - sum;
     item0 += run_items - n;
     int mine = -1;
-    int64_t start = 0, first = 0;
+    int64_t start = 0;
+    int32_t first = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (at <= walk.from && walk.from < at + span[j]) mine = s0 + j, start = at, first = item0;
@@ -398,12 +429,11 @@ __device__ __noinline__ void note_segments(const AttentionParams& p) {
   for (int s0 = 0; s0 < b.groups + b.sequences; s0 += 32) {
     const int s = s0 + lane;
     int32_t n = 0;
-    if (s < b.groups) {
-      n = segment(p, s, 0).items;
-      over |= b.prefix_lens[s] > 0 && b.prefix_lens[s] > far_len(p, s);
-    } else if (s < b.groups + b.sequences) {
-      const int len = b.lens[s - b.groups];
-      over |= len > 0 && len > own_len(p, s - b.groups);
+    if (s < b.groups + b.sequences) {
+      const Raw raw = raw_segment(b, s, true);
+      if (s < b.groups) n = segment_of(p, s, raw).items;
+      over |= raw.len > 0 && raw.len > capped(p, raw.len, s < b.groups ? b.prefix_width
+                                                                       : b.table_width);
     }
     int32_t sum = n;
 #pragma unroll
@@ -1197,8 +1227,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- joining the parts ------------------------------------------------------------
 
-constexpr int kJoinWarps = 4;
-constexpr int kJoinThreads = kJoinWarps * 32;
 
 // Where a row's results lie in a segment's parts: for k < n in row place + k / teams *
 // part_rows + k % teams * team_rows (a part has the row once, or for each of the
@@ -1236,10 +1264,10 @@ __device__ __forceinline__ Side side_of(const AttentionParams& p, bool far, int 
 // One CTA a row and query head: over the parts of its prefix and its own tokens,
 // out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i, in a fixed order.  A thread a
 // part for the weights, then a warp a part for the values, four parts in flight.
-template <int DIM>
-__global__ void __launch_bounds__(kJoinThreads)
+template <int DIM, int kJoinWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32)
     join_kernel(const __grid_constant__ AttentionParams p) {
-  constexpr int E = DIM / 32;
+  constexpr int E = DIM / 32, kJoinThreads = kJoinWarps * 32;
   __shared__ float weight[kJoinThreads];
   __shared__ const float* source[kJoinThreads];
   __shared__ float values[kJoinWarps][DIM];
@@ -1255,7 +1283,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   far.n = own.n = 0;
   const int fresh = fresh_of(b, seq);
   if (i < fresh) {
-    if (own_len(p, seq) > 0)
+    if (b.lens[seq] > 0)
       own = side_of(p, false, p.seq_rows, in_seq, kvh, (int64_t)seq * p.ws.own_items);
     for (int g0 = 0; g0 < b.groups; g0 += 32) {
       const int g = g0 + lane;
@@ -1356,8 +1384,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
   uint16_t* out = static_cast<uint16_t*>(p.out.data) + (int64_t)token * p.out.token_stride +
                   (int64_t)head * p.out.head_stride;
-  if (threadIdx.x < DIM / 2) {
-    const int e = 2 * (int)threadIdx.x;
+  for (int e = 2 * (int)threadIdx.x; e < DIM; e += 2 * kJoinThreads) {
     float lo = 0.f, hi = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) lo += values[w][e], hi += values[w][e + 1];
@@ -1392,11 +1419,17 @@ cudaError_t launch_dim(const AttentionParams& p, const PageMaps& maps, cudaStrea
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attention_kernel<DIM>, p, maps);
   if (e != cudaSuccess) return e;
+  // Eight warps a row and head while those are few and have many parts each; else
+  // two, which all fit on the device at once (2048 rows and heads: 4.7 us a call
+  // less than with four).
+  const int64_t outputs = (int64_t)p.batch.sequences * p.batch.chunk * p.heads;
+  const int warps = outputs <= 4 * p.ctas ? 8 : 2;
   cfg.gridDim =
       dim3((unsigned)(p.batch.sequences * p.batch.chunk), (unsigned)p.heads);  // <= 2^24, 2^12
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.blockDim = dim3((unsigned)(32 * warps));
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<DIM>, p);
+  return warps == 8 ? cudaLaunchKernelEx(&cfg, join_kernel<DIM, 8>, p)
+                    : cudaLaunchKernelEx(&cfg, join_kernel<DIM, 2>, p);
 }
 
 uint64_t up256(uint64_t x) { return (x + 255) & ~255ull; }
