@@ -139,12 +139,15 @@ struct Raw {
   int len, first, end;   // first sequence of a prefix and the one behind its last; or
                          // 0 and the sequence's new tokens
 };
-__device__ __forceinline__ Raw raw_segment(const BatchView& b, int s, bool in) {
+// dry: made up, nothing is read.
+__device__ __forceinline__ Raw raw_segment(const BatchView& b, int s, bool in, bool dry) {
   const bool far = s < b.groups;
   const int seq = far ? 0 : s - b.groups;
   Raw r;
-  r.len = r.first = 0;
+  r.len = in && dry ? 3 * kKvTile : 0;
+  r.first = 0;
   r.end = 1;
+  in = in && !dry;
   if (in) r.len = *(far ? b.prefix_lens + s : b.lens + seq);
   if (in && far) r.first = b.group_start[s];
   if (in && (far || b.q_lens)) r.end = *(far ? b.group_start + s + 1 : b.q_lens + seq);
@@ -218,12 +221,13 @@ struct Walk {
   bool open;         // the segment has been looked up
   Segment g;
   At at, end;        // its tiles left
+  bool dry;          // a rehearsal: see raw_segment
   __device__ __forceinline__ bool next(const AttentionParams& p, Part& part) {
     const int segments = p.batch.groups + p.batch.sequences;
     for (;;) {
       if (!open) {
         if (s >= segments || start >= to) return false;
-        g = segment_of(p, s, raw_segment(p.batch, s, true));
+        g = segment_of(p, s, raw_segment(p.batch, s, true, dry));
         price(p, g, cap);
         at.item = at.tile = 0;
         end.item = g.tiles ? g.items : 0;
@@ -319,7 +323,7 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 // may be without a tile (the join counts on it), so a share is at least as long as
 // the widest gap between two tiles' starts, the most that a tile costs plus a lead:
 // leads are capped for it, and where that leaves none every tile costs 1.
-__device__ __forceinline__ Walk share_out(const AttentionParams& p) {
+__device__ __forceinline__ Walk share_out(const AttentionParams& p, bool dry) {
   const BatchView& b = p.batch;
   const int segments = b.groups + b.sequences;
   const int lane = threadIdx.x & 31;
@@ -328,7 +332,7 @@ __device__ __forceinline__ Walk share_out(const AttentionParams& p) {
   auto take = [&](int s0) {
     Raw raw[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) raw[j] = raw_segment(b, s0 + j, s0 + j < segments);
+    for (int j = 0; j < 4; ++j) raw[j] = raw_segment(b, s0 + j, s0 + j < segments, dry);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       g[j] = segment_of(p, s0 + j, raw[j]);
@@ -369,6 +373,7 @@ __device__ __forceinline__ Walk share_out(const AttentionParams& p) {
   walk.s = segments;
   walk.start = walk.item0 = 0;
   walk.open = false;
+  walk.dry = dry;
   int64_t run = 0;
   int32_t run_items = 0;
 #pragma unroll 1
@@ -430,7 +435,7 @@ __device__ __noinline__ void note_segments(const AttentionParams& p) {
     const int s = s0 + lane;
     int32_t n = 0;
     if (s < b.groups + b.sequences) {
-      const Raw raw = raw_segment(b, s, true);
+      const Raw raw = raw_segment(b, s, true, false);
       if (s < b.groups) n = segment_of(p, s, raw).items;
       over |= raw.len > 0 && raw.len > capped(p, raw.len, s < b.groups ? b.prefix_width
                                                                        : b.table_width);
@@ -458,14 +463,23 @@ __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* maps, ui
   const int page = 1 << p.cache.page_shift;
   const int mine = lane / kHalves, half = lane % kHalves;   // this lane's box and half of it
   const BatchView& b = p.batch;
-  Walk walk = share_out(p);
+  // The way to the first part twice: a rehearsal, while the previous kernel ends, that
+  // brings its instructions into the cache (cold, they took 10,000 cycles), then in
+  // earnest.
+  Walk walk;
+  Part part;
+  bool more = false;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1) wait_prerequisites();
+    walk = share_out(p, pass == 0);
+    part.n = 0;
+    part.kind = kOne;
+    more = walk.next(p, part);
+  }
   uint32_t seq = 0;
   bool ok = true;
   for (uint32_t k = 0; ok; ++k) {
-    Part part;
-    part.n = 0;
-    part.kind = kOne;
-    const bool more = walk.next(p, part);
     const uint32_t e = k % kQueue, turn = k / kQueue;
     if (turn) ok = __all_sync(kAll, wait(&bars->heard[e], (turn - 1) & 1u, ctl));
     if (!ok) break;
@@ -526,6 +540,9 @@ __device__ void produce_kv(const AttentionParams& p, const CUtensorMap* maps, ui
       }
       if (!ok) break;
     }
+    part.n = 0;
+    part.kind = kOne;
+    more = walk.next(p, part);
   }
   // No CTA leaves while its copies run.
   const WaitCtl dc = drain_ctl_default(p.cache.err);
@@ -1208,7 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  wait_prerequisites();
+  if (warp != kProducerWarp) wait_prerequisites();
   const Ctl ctl{p.cache.err, p.wait_limit ? p.wait_limit : kDefaultWaitLimit, &bars->abort};
   if (warp < 8) {
     softmax_team<DIM>(p, smem, bars, ctl, (uint32_t)(warp >> 2));
