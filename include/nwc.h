@@ -468,8 +468,9 @@ nwc_status nwc_kv_attention_workspace(const nwc_kv_cache* cache, const nwc_kv_ba
  * A row that sees no token, and a padding row, is zero with d_lse -infinity.
  * Scores, sums and the running maximum are FP32; a probability is rounded to
  * BF16 before it multiplies V.  Memory behind a sequence's or a prefix's last
- * token is not used, whatever it holds.  The result is the same bit pattern on
- * every run.
+ * token is not used, whatever it holds; but a V that is not finite, of a call's new
+ * token, may reach the rows before it in the same call.  The result is the same bit
+ * pattern on every run.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA (launch). */
 nwc_status nwc_kv_attention(const nwc_kv_cache* cache, const nwc_kv_batch* batch,
                             const nwc_heads* q, int32_t heads, float scale,

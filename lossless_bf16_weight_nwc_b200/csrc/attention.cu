@@ -271,12 +271,13 @@ struct Walk {
 struct Ctl {
   uint32_t* err;
   uint32_t limit;
+  bool test;   // a limit set by a test: polls that do not themselves wait
   volatile uint32_t* abort;
 };
 // False (and every role leaves) when a wait gave up here or elsewhere.
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, const Ctl& c) {
   for (uint32_t it = 0; it < c.limit; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (c.test ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
     if (*c.abort) return false;
   }
   *c.abort = 1u;
@@ -284,7 +285,7 @@ __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, const Ctl& 
   return false;
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Ctl& c) {
-  return mbar_try_wait(bar, parity) || wait_on(bar, parity, c);
+  return (!c.test && mbar_try_wait(bar, parity)) || wait_on(bar, parity, c);
 }
 
 // ---- roles ---------------------------------------------------------------------
@@ -1226,7 +1227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp != kProducerWarp) wait_prerequisites();
-  const Ctl ctl{p.cache.err, p.wait_limit ? p.wait_limit : kDefaultWaitLimit, &bars->abort};
+  const Ctl ctl{p.cache.err, p.wait_limit ? p.wait_limit : kDefaultWaitLimit,
+                p.wait_limit != 0, &bars->abort};
   if (warp < 8) {
     softmax_team<DIM>(p, smem, bars, ctl, (uint32_t)(warp >> 2));
   } else if (warp == kProducerWarp) {
@@ -1269,11 +1271,14 @@ __device__ __forceinline__ Side side_of(const AttentionParams& p, bool far, int 
   d.n = 0;
   d.place = 0;
   const int64_t slots = far ? p.ws.far_slots : p.ws.own_slots;
-  if (item < slots - p.ctas) {
+  if (0 <= item && item < slots - p.ctas) {
     const int2 span = *reinterpret_cast<const int2*>(
         p.workspace + (far ? p.ws.far_spans : p.ws.own_spans) + 8 * item);
-    d.n = (span.y - span.x + 1) * d.teams;
-    d.place = (item + span.x) * d.part_rows + at;
+    // (After a wait that gave up, what is there may be anything.)
+    if (0 <= span.x && span.x <= span.y && span.y < p.ctas) {
+      d.n = (span.y - span.x + 1) * d.teams;
+      d.place = (item + span.x) * d.part_rows + at;
+    }
   }
   return d;
 }

@@ -242,6 +242,70 @@ def test_append(paged, lens, chunk, q_lens, kw, tin, inter):
     assert c.kv.device_error() == (0, 0)
 
 
+def test_append_large_batches_and_heads(paged):
+    """More tokens than fill the device, heads that do not fill a warp's group."""
+    for seqs, h, hk, dim in ((1500, 5, 1, 64), (1300, 3, 3, 80), (1250, 2, 1, 256)):
+        c = Case(paged, seqs, [1 + i % 20 for i in range(seqs)], kv_heads=hk, dim=dim,
+                 poison=False)
+        y = randn(c.g, seqs, h + 2 * hk, dim).bfloat16()
+        q, k, v = y.split([h, hk, hk], 1)
+        freq = paged.rope_frequencies(dim // 16 * 16, 1e4)
+        got = c.kv.append(c.batch, k, v, q=q, freq=freq)
+        pos = torch.tensor(c.lens, device="cuda") - 1
+        want, bound = ref.norm_rotate(q, None, pos, freq, False, 0)
+        assert ref.close(got, want, bound, torch.bfloat16)
+        at = (c.table[torch.arange(seqs, device="cuda"), pos // 16].long(), pos % 16)
+        want, bound = ref.norm_rotate(k, None, pos, freq, False, 0)
+        assert ref.close(c.k[at], want, bound, torch.bfloat16)
+        assert torch.equal(c.v[at], v)
+
+
+def test_append_in_place(paged):
+    c = Case(paged, 15, [9, 30], poison=False)
+    q, k, v = (randn(c.g, 2, n, 64).bfloat16() for n in (6, 2, 2))
+    freq = paged.rope_frequencies(64, 1e4)
+    want, bound = ref.norm_rotate(q, None, ints([8, 29]), freq, True, 0)
+    assert c.kv.append(c.batch, k, v, q=q, freq=freq, interleaved=True, q_out=q) is q
+    assert ref.close(q, want, bound, torch.bfloat16)
+
+
+def test_refusals_on_the_device(paged):
+    """What the Python calls refuse with tensors on the device."""
+    c = Case(paged, 16, [9, 30], poison=False)
+    q, k, v = (randn(c.g, 2, n, 64) for n in (4, 2, 2))
+    freq = paged.rope_frequencies(64, 1e4)
+    append, attend = c.kv.append, c.kv.attend
+    for bad in (lambda: append(c.batch, k[:1], v[:1]), lambda: append(c.batch, k, v.bfloat16()),
+                lambda: append(c.batch, k, v[:, :1]), lambda: append(c.batch, k, v, q=q.half()),
+                lambda: append(c.batch, k, v, q_out=q), lambda: append(c.batch, k, v, freq=freq[:30]),
+                lambda: append(c.batch, k, v, q=q, q_out=q), lambda: append(c.batch, k.cpu(), v),
+                lambda: append(c.batch, k, v, q_weight=torch.ones(32, device="cuda")),
+                lambda: append(c.lens, k, v), lambda: attend(c.batch, q),
+                lambda: attend(c.batch, q.bfloat16()[:, :3]),
+                lambda: attend(c.batch, q.bfloat16()[:1]),
+                lambda: attend(c.batch, torch.zeros(2 * 4 * 64 + 4, device="cuda").bfloat16()[4:]
+                               .view(2, 4, 64)),
+                lambda: attend(c.batch, q.bfloat16(), out=torch.empty_like(q)),
+                lambda: attend(c.batch, q.bfloat16(), out=q.bfloat16()[:1].expand(2, 4, 64)),
+                lambda: paged.PagedKV(c.k[:, :12], c.v[:, :12]),
+                lambda: paged.PagedKV(c.k.float(), c.v.float()),
+                lambda: paged.PagedKV(c.k, c.v[:1]), lambda: paged.PagedKV(c.k[..., 1:], c.v[..., 1:]),
+                lambda: paged.PagedBatch(c.table, ints([1])),
+                lambda: paged.PagedBatch(c.table.long(), ints([1, 2])),
+                lambda: paged.PagedBatch(c.table, ints([1, 2]), prefix_table=c.table),
+                lambda: paged.qk_norm_rope(q, k.bfloat16(), ints([1, 2]), freq),
+                lambda: paged.qk_norm_rope(q, k, ints([1]), freq),
+                lambda: paged.qk_norm_rope(q, k, ints([1, 2]), freq, out=(q, None))):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
+    leaf = q.clone().requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        append(c.batch, k, v, q=leaf)
+    with torch.no_grad():
+        append(c.batch, k, v, q=leaf)
+    assert c.kv.device_error() == (0, 0)
+
+
 def test_append_without_q_or_rotation(paged):
     c = Case(paged, 4, [4, 9], poison=False)
     k, v = randn(c.g, 2, 2, 64), randn(c.g, 2, 2, 64)
@@ -296,6 +360,15 @@ ATTEND = [  # lens, chunk, q_lens, heads, kw
     ([100, 20], 1, None, 128, dict(kv_heads=1, dim=128)),
     ([300], 3, None, 256, dict(kv_heads=2, dim=64)),
     ([20000], 64, None, 8, dict(kv_heads=2, dim=128, page=64)),
+    # Heads that come by eight, four, two and one to a tile, rows up to and over 16.
+    ([130, 1, 17, 300], 1, None, 48, dict(kv_heads=16, page=8)),
+    ([130, 0, 17, 300], 3, [3, 1, 2, 3], 24, dict(kv_heads=12, dim=128, page=128)),
+    ([900, 64, 33], 1, None, 72, dict(kv_heads=6, page=16, prefix=[65], starts=[1, 3])),
+    ([900, 64, 33], 4, None, 12, dict(kv_heads=3, dim=128, page=8, prefix=[131], starts=[0, 2])),
+    ([500, 77], 1, None, 12, dict(kv_heads=1, dim=128, page=64)),
+    ([500, 77], 17, [17, 5], 3, dict(kv_heads=3, page=32)),
+    ([1300], 5, None, 13, dict(kv_heads=1, page=16, prefix=[3], starts=[0, 1])),
+    ([33, 65, 129] * 3, 1, None, 8, dict(kv_heads=8, dim=128, page=256)),
     # Long and short shares of every kind of rows in turn, many parts an SM.
     ([7 * i % 500 + 1 for i in range(64)], 1, None, 32,
      dict(kv_heads=8, dim=128, prefix=[8200], starts=[0, 64])),
@@ -376,6 +449,49 @@ def test_attend_missing_pages(paged):
     got = c.kv.attend(over, q[1:])
     assert c.kv.device_error() == (1, 4)
     assert ref.close(got, want[1:], bound[1:], torch.bfloat16)
+
+
+def test_attend_bounded_waits(paged):
+    """With a limit of one poll the kernel's waits give up: it returns, says so, and
+    the next call is right."""
+    from lossless_bf16_weight_nwc_b200 import _lib
+    c = Case(paged, 12, [300] * 6, dim=128, kv_heads=4, prefix=[900], starts=[0, 6])
+    q = randn(c.g, 6, 32, 128).bfloat16()
+    _lib.nwc_test_set_wait_limit(1)
+    try:
+        c.kv.attend(c.batch, q)
+        status, word = c.kv.device_error()
+    finally:
+        _lib.nwc_test_set_wait_limit(0)
+    assert (status, word & 1) == (6, 1)                  # NWC_ERR_DEVICE_TIMEOUT
+    got, lse = c.kv.attend(c.batch, q, return_lse=True)
+    c.check(q, got, lse)
+
+
+def test_attend_unordered_groups(paged):
+    """Group starts that are not ascending or point outside: some answer, nothing
+    written out of bounds, and the rows outside such groups are right."""
+    c = Case(paged, 13, [40] * 8, prefix=[500, 300, 100], starts=[0, 2, 4, 8])
+    q = randn(c.g, 8, 4, 64).bfloat16()
+    for starts in ([4, 2, 9, 1], [-3, 0, 100, 100], [8, 8, 8, 8], [0, 8, 0, 8]):
+        batch = paged.PagedBatch(c.table, ints(c.lens), None, c.far, ints(c.prefix), ints(starts))
+        out = torch.full((10, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        c.kv.attend(batch, q, out=out[1:9])
+        assert bool((out[[0, 9]] == 7).all())
+        c.kv.device_error()
+    got, lse = c.kv.attend(c.batch, q, return_lse=True)
+    c.check(q, got, lse)
+
+
+def test_attend_shared_pages_and_repeats(paged):
+    """Sequences that point at the same pages, and a prefix whose pages repeat."""
+    c = Case(paged, 14, [64, 64, 64], prefix=[64], starts=[0, 3], poison=False)
+    c.table[1] = c.table[0]
+    c.table[2, :4] = c.table[0, 0]
+    c.far[0, :4] = c.far[0, 1]
+    q = randn(c.g, 3, 8, 64).bfloat16()
+    got, lse = c.kv.attend(c.batch, q, return_lse=True)
+    c.check(q, got, lse)
 
 
 def test_attend_strides(paged):
