@@ -1,4 +1,6 @@
-// ptx.cuh — inline PTX and the bounded mbarrier wait that the sm_100a kernels share.
+// ptx.cuh — inline PTX and the bounded mbarrier wait of the paged kernels.  (kernels.cu
+// has those it uses itself: the DRAM traffic that the benchmark reports for it was
+// captured for exactly its text.)
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -34,20 +36,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bulk copy global -> this CTA's shared memory, completion counted in bytes on
-// `bar`.  Plain (non-multicast) form.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-// Hint: bring `bytes` (a multiple of 16) of global memory into L2.
-__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void fence_barrier_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
@@ -68,16 +56,6 @@ inline __device__ bool wait_bounded(uint64_t* bar, uint32_t parity, const WaitCt
   return false;
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
 // Programmatic dependent launch: let the next kernel on the stream start its
 // prologue now (its CTAs become resident as this grid's CTAs exit), and wait until
 // the previous kernel has completed and its writes are visible.
@@ -87,9 +65,6 @@ __device__ __forceinline__ void allow_dependents() {
 __device__ __forceinline__ void wait_prerequisites() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
-__device__ __forceinline__ void named_barrier_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -97,20 +72,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "r"(addr));
   return v;
 }
-// v = [addr] when `need` is non-zero, else v is left as it was (predicated
-// load, no branch).
-__device__ __forceinline__ void lds32_keep(uint32_t& v, uint32_t addr, uint32_t need) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.shared.u32 %0, [%1];\n\t}"
-               : "+r"(v)
-               : "r"(addr), "r"(need));
-}
-// Low word of ({hi, lo} >> (n mod 32)).
-__device__ __forceinline__ uint32_t shr_wrap(uint32_t lo, uint32_t hi, uint32_t n) {
-  uint32_t r;
-  asm("shf.r.wrap.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(lo), "r"(hi), "r"(n));
-  return r;
-}
-
 // D += A B on the tensor cores, one warp: A is 16 x 16 BF16 (row-major
 // fragment a0..a3), B is 16 x 8 BF16 (column-major fragment b0, b1), D is
 // 16 x 8 FP32 (d0..d3).  Fragment of lane L (g = L / 4, c = L % 4):
@@ -184,31 +145,6 @@ __device__ __forceinline__ constexpr uint32_t umma_idesc_bf16(int m, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
 }
-// D[tmem] (+)= A B, issued by one thread.
-__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// `bar` completes one phase when every tcgen05 operation this thread issued
-// before has completed.
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
-}
-// 2-D TMA load (tile mode, no multicast) of the box at (c0, c1) into `dst`.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t c0,
-                                            int32_t c1, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                        uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
@@ -219,27 +155,6 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 // (lane base + l), v[k] = column (col + k), as FP32.
 template <int NCOL>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[NCOL]);
-template <>
-__device__ __forceinline__ void tmem_load<4>(uint32_t taddr, float (&v)[4]) {
-  uint32_t r[4];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(r[k]);
-}
-template <>
-__device__ __forceinline__ void tmem_load<8>(uint32_t taddr, float (&v)[8]) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                 "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[k]);
-}
 template <>
 __device__ __forceinline__ void tmem_load<16>(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
@@ -255,10 +170,9 @@ __device__ __forceinline__ void tmem_load<16>(uint32_t taddr, float (&v)[16]) {
   for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
 }
 
-// The same product, and one with A in TMEM (BF16, two of K a column), executed by
-// a whole warp and issued by the lane whose `leader` is non-zero (always the
-// same one): without a branch around them their operands stay in uniform
-// registers.
+// D[tmem] (+)= A B, and the same with A in TMEM (BF16, two of K a column), executed by
+// a whole warp and issued by the lane whose `leader` is non-zero (always the same
+// one): without a branch around them their operands stay in uniform registers.
 __device__ __forceinline__ void umma_bf16_by(uint32_t leader, uint32_t d_tmem, uint64_t a_desc,
                                              uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
