@@ -19,16 +19,27 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
 from . import _lib
 
-# The C calls themselves: _lib's wrappers also take tensors, which costs a call 1 us.
-_LIB, _check = _lib.LIB, _lib._check
+# The calls' structures are packed here and passed as addresses, which takes half as
+# long as filling _lib's ctypes structures: for one token a call is bound by the host.
+_RAW = ctypes.CDLL(_lib.LIB_PATH)
+_P, _I = ctypes.c_void_p, ctypes.c_int32
+_RAW.nwc_qk_norm_rope.argtypes = [_P] * 4 + [_I] * 4 + [_P, _I, _P, _P]
+_RAW.nwc_kv_append.argtypes = [_P] * 4 + [_I] + [_P] * 4
+_RAW.nwc_kv_attention.argtypes = [_P, _P, _P, _I, ctypes.c_float, _P, _P, _P, ctypes.c_uint64, _P]
+_check = _lib._check
 _TYPES = {torch.bfloat16: _lib.NWC_TYPE_BF16, torch.float32: _lib.NWC_TYPE_F32}
 _HEADS = ctypes.sizeof(_lib.nwc_heads)
 _ROPE = ctypes.sizeof(_lib.nwc_rope)
+_pack_heads = struct.Struct("@IIPqq").pack
+_pack_rope = struct.Struct("@IiiIPPPf0P").pack
+assert len(_pack_heads(0, 0, 0, 0, 0)) == _HEADS
+assert len(_pack_rope(0, 0, 0, 0, 0, 0, 0, 0)) == _ROPE
 _POSITIONS = (torch.int32, torch.int64)
 _BF16 = (torch.bfloat16,)
 _F64 = (torch.float64,)
@@ -59,9 +70,11 @@ def _no_grad(*tensors) -> None:
                                  "give; call under torch.no_grad()")
 
 
-def _heads(t, what: str, shape, device, dtypes=_TYPES):
+def _heads(t, what: str, shape, device, dtypes=_TYPES, wide: bool = False,
+           output: bool = False) -> bytes:
     """The C view of a tensor [tokens, heads, dim] with any strides but a
-    contiguous last dimension."""
+    contiguous last dimension; wide: moved 16 bytes at a time; output: no two
+    elements at one place."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
     dtype = t.dtype
@@ -74,25 +87,26 @@ def _heads(t, what: str, shape, device, dtypes=_TYPES):
         raise ValueError(f"{what}: the last dimension must be contiguous")
     if t.device != device:
         raise ValueError(f"{what}: on {t.device}, expected {device}")
-    return _lib.nwc_heads(_HEADS, _TYPES[dtype], t.data_ptr(), ts if shape[0] > 1 else 0,
-                          hs if shape[1] > 1 else 0)
-
-
-def _output(t, what: str, shape, device, dtypes):
-    h = _heads(t, what, shape, device, dtypes)
-    rows, heads, dim = shape
-    ts, hs = h.token_stride, h.head_stride
-    if not ((heads == 1 or hs >= dim) and (rows == 1 or ts >= dim) and
-            (heads == 1 or rows == 1 or ts >= heads * hs or hs >= rows * ts)) and rows:
+    tokens, heads, dim = shape
+    if tokens < 2:
+        ts = 0
+    if heads < 2:
+        hs = 0
+    at = t.data_ptr()
+    if wide and tokens and (at % 16 or ts % 8 or hs % 8):
+        raise ValueError(f"{what}: needs 16-byte alignment and strides of multiples of 8 elements")
+    if output and tokens and not (
+            (heads < 2 or hs >= dim) and (tokens < 2 or ts >= dim) and
+            (heads < 2 or tokens < 2 or ts >= heads * hs or hs >= tokens * ts)):
         raise ValueError(f"{what}: its elements overlap")
-    return h
+    return _pack_heads(_HEADS, _TYPES[dtype], at, ts, hs)
 
 
 def _new(like, shape):
     """A new BF16 tensor of the shape of `like`, [tokens, heads, dim], and its C view."""
     t = torch.empty_like(like, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
     dim = shape[2]
-    return t, _lib.nwc_heads(_HEADS, 0, t.data_ptr(), shape[1] * dim, dim)
+    return t, _pack_heads(_HEADS, 0, t.data_ptr(), shape[1] * dim, dim)
 
 
 def _vector(t, what: str, device, n: int, dtypes) -> int:
@@ -111,7 +125,7 @@ def _vector(t, what: str, device, n: int, dtypes) -> int:
 def _rope(dim: int, device, freq, q_weight, k_weight, eps: float, interleaved: bool):
     if not 0 <= eps < math.inf:
         raise ValueError("eps: a finite number, not negative")
-    n, d_freq, d_q, d_k, kind = 0, None, None, None, 0
+    n, d_freq, d_q, d_k, kind = 0, 0, 0, 0, 0
     if freq is not None:
         n = freq.numel() if isinstance(freq, torch.Tensor) else 0
         d_freq = _vector(freq, "freq", device, n, _F64)
@@ -125,7 +139,7 @@ def _rope(dim: int, device, freq, q_weight, k_weight, eps: float, interleaved: b
             raise TypeError("q_weight and k_weight: expected one dtype")
         d_k = _vector(k_weight, "k_weight", device, dim, _TYPES)
         kind = _TYPES[k_weight.dtype]
-    return _lib.nwc_rope(_ROPE, 2 * n, interleaved, kind, d_freq, d_q, d_k, eps)
+    return _pack_rope(_ROPE, 2 * n, interleaved, kind, d_freq, d_q, d_k, eps)
 
 
 class _On:
@@ -153,31 +167,20 @@ class _On:
         return self.context.__exit__(*args)
 
 
-class _Here:
-    """_On for the current device's current stream, which needs no switch."""
-
-    def __init__(self, raw: int):
-        self.raw = raw
-
-    def __enter__(self):
-        return self.raw
-
-    def __exit__(self, *args):
-        return None
-
-
-def _on(device, stream):
-    if stream is None and torch.cuda.current_device() == device.index:
-        return _Here(_raw_stream(device.index))
-    return _On(device, stream)
-
-
 def _raw_stream(index: int) -> int:
     return torch.cuda.current_stream(index).cuda_stream
 
 
 # The same handle without building a torch.cuda.Stream (3 us less a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _on(device, stream, call):
+    """call(raw stream) where it should run."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(_raw_stream(device.index))
+    with _On(device, stream) as raw:
+        return call(raw)
 
 
 def _cuda(t, what: str):
@@ -215,7 +218,8 @@ def qk_norm_rope(q, k, positions, freq=None, q_weight=None, k_weight=None, eps: 
         kh = _heads(k, "k", (tokens, kv_heads, dim), device, (first.dtype,))
     rope = _rope(dim, device, freq, q_weight, k_weight, eps, interleaved)
     at = _vector(positions, "positions", device, tokens, _POSITIONS)
-    with _on(device, stream) as raw:
+
+    def call(raw):
         qo = ko = qoh = koh = None
         if out is None:
             if q is not None:
@@ -228,15 +232,17 @@ def qk_norm_rope(q, k, positions, freq=None, q_weight=None, k_weight=None, eps: 
                 raise ValueError("out: a pair of tensors for q and k, None where the input is "
                                  "None")
             if q is not None:
-                qoh = _output(qo, "out[0]", (tokens, heads, dim), device, _TYPES)
+                qoh = _heads(qo, "out[0]", (tokens, heads, dim), device, output=True)
             if k is not None:
-                koh = _output(ko, "out[1]", (tokens, kv_heads, dim), device,
-                              _TYPES if q is None else (qo.dtype,))
+                koh = _heads(ko, "out[1]", (tokens, kv_heads, dim), device,
+                             _TYPES if q is None else (qo.dtype,), output=True)
         if tokens:
-            _check(_LIB.nwc_qk_norm_rope(qh, kh, qoh, koh, tokens, heads, kv_heads, dim, at,
+            _check(_RAW.nwc_qk_norm_rope(qh, kh, qoh, koh, tokens, heads, kv_heads, dim, at,
                                          positions.dtype == torch.int64, rope, raw),
                    "nwc_qk_norm_rope")
-    return qo, ko
+        return qo, ko
+
+    return _on(device, stream, call)
 
 
 class PagedBatch:
@@ -279,7 +285,7 @@ class PagedBatch:
                    *shared,
                    _vector(prefix_lens, "prefix_lens", self.device, self.groups, i32))
         self._fields = (*table, lens, fresh, *far)
-        self._views = {}
+        self._views, self._structs = {}, []
 
     def _table(self, t, what: str):
         if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 2:
@@ -291,7 +297,7 @@ class PagedBatch:
         return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.shape[1]
 
     def _view(self, rows: int):
-        """The C view for calls of `rows` rows in all."""
+        """The address of the C view for calls of `rows` rows in all."""
         view = self._views.get(rows)
         if view is None:
             chunk = rows // self.sequences if self.sequences else 1
@@ -300,9 +306,10 @@ class PagedBatch:
                                  "at least one, for each")
             if rows > 1 << 24:
                 raise ValueError(f"{rows} rows; a call takes up to 2^24")
-            view = _lib.nwc_kv_batch(ctypes.sizeof(_lib.nwc_kv_batch), self.sequences, chunk,
-                                     *self._fields)
-            self._views[rows] = view
+            fields = _lib.nwc_kv_batch(ctypes.sizeof(_lib.nwc_kv_batch), self.sequences, chunk,
+                                       *self._fields)
+            self._structs.append(fields)
+            view = self._views[rows] = ctypes.addressof(fields)
         return view
 
 
@@ -346,6 +353,7 @@ class PagedKV:
         self._view = _lib.nwc_kv_cache(ctypes.sizeof(_lib.nwc_kv_cache), self.page_size,
                                        self.kv_heads, self.dim, self.pages, k_pages.data_ptr(),
                                        v_pages.data_ptr(), *strides, self._error.data_ptr())
+        self._at = ctypes.addressof(self._view)
         self._workspace = {}
 
     def device_error(self, stream=None) -> tuple[int, int]:
@@ -380,7 +388,7 @@ class PagedKV:
         kh = _heads(k, "k", shape, device)
         same = (k.dtype,)
         vh = _heads(v, "v", shape, device, same)
-        heads, qh, qoh = 1, None, None
+        heads, qh = 1, None
         if q is not None:
             if not isinstance(q, torch.Tensor) or q.dim() != 3:
                 raise ValueError("q: expected a tensor [rows, heads, dim]")
@@ -390,15 +398,18 @@ class PagedKV:
         elif q_out is not None:
             raise ValueError("q_out: given without q")
         rope = _rope(self.dim, device, freq, q_weight, k_weight, eps, interleaved)
-        with _on(device, stream) as raw:
+
+        def call(raw, q_out=q_out, qoh=None):
             if q_out is not None:
-                qoh = _output(q_out, "q_out", shape, device, _BF16)
+                qoh = _heads(q_out, "q_out", shape, device, _BF16, output=True)
             elif q is not None:
                 q_out, qoh = _new(q, shape)
             if rows:
-                _check(_LIB.nwc_kv_append(self._view, view, qh, qoh, heads, kh, vh, rope, raw),
+                _check(_RAW.nwc_kv_append(self._at, view, qh, qoh, heads, kh, vh, rope, raw),
                        "nwc_kv_append")
-        return q_out
+            return q_out
+
+        return _on(device, stream, call)
 
     def attend(self, batch: PagedBatch, q, scale: float | None = None, out=None,
                return_lse: bool = False, stream=None):
@@ -415,31 +426,33 @@ class PagedKV:
         if heads < 1 or heads % self.kv_heads:
             raise ValueError(f"q: {heads} heads, expected a multiple of {self.kv_heads}")
         shape = (rows, heads, self.dim)
-        qh = _heads(q, "q", shape, self.device, _BF16)
-        if rows and (qh.d_data % 16 or qh.token_stride % 8 or qh.head_stride % 8):
-            raise ValueError("q: needs 16-byte alignment and strides of multiples of 8 elements")
+        qh = _heads(q, "q", shape, self.device, _BF16, wide=True)
         if scale is None:
             scale = self.dim ** -0.5
-        with _on(self.device, stream) as raw:
+
+        def call(raw, out=out):
             if out is None:
                 out, oh = _new(q, shape)
             else:
-                oh = _output(out, "out", shape, self.device, _BF16)
+                oh = _heads(out, "out", shape, self.device, _BF16, wide=True, output=True)
             lse = torch.empty((rows, heads), dtype=torch.float32,
                               device=self.device) if return_lse else None
             if rows:
                 key = (rows, batch.sequences, batch.groups, heads)
                 need = self._workspace.get(key)
                 if need is None:
-                    need = _lib.nwc_kv_attention_workspace(self._view, view, heads)
+                    need = _lib.nwc_kv_attention_workspace(
+                        self._view, _lib.nwc_kv_batch.from_address(view), heads)
                     self._workspace[key] = need
                 # From torch's allocator on the call's stream: calls on different
                 # streams, and captured graphs, each have their own.
                 ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-                _check(_LIB.nwc_kv_attention(self._view, view, qh, heads, scale, oh,
+                _check(_RAW.nwc_kv_attention(self._at, view, qh, heads, scale, oh,
                                              None if lse is None else lse.data_ptr(),
                                              ws.data_ptr(), need, raw), "nwc_kv_attention")
-        return (out, lse) if return_lse else out
+            return (out, lse) if return_lse else out
+
+        return _on(self.device, stream, call)
 
 
 class AttentionBlock:

@@ -161,9 +161,14 @@ def test_tensor_checks(lib):
     from lossless_bf16_weight_nwc_b200 import paged
     cpu = torch.device("cpu")
     t = torch.zeros(3, 4, 64)
-    v = paged._heads(t, "t", (3, 4, 64), cpu)
-    assert (v.type, v.token_stride, v.head_stride) == (1, 256, 64)
-    assert paged._heads(t[:1], "t", (1, 4, 64), cpu).token_stride == 0
+
+    def view(*args, **kw):
+        return lib.nwc_heads.from_buffer_copy(paged._heads(*args, **kw))
+
+    v = view(t, "t", (3, 4, 64), cpu)
+    assert (v.struct_size, v.type, v.d_data) == (ctypes.sizeof(v), 1, t.data_ptr())
+    assert (v.token_stride, v.head_stride) == (256, 64)
+    assert view(t[:1], "t", (1, 4, 64), cpu).token_stride == 0
     with pytest.raises(TypeError):
         paged._heads(t.half(), "t", (3, 4, 64), cpu)
     with pytest.raises(ValueError, match="shape"):
@@ -172,14 +177,22 @@ def test_tensor_checks(lib):
         paged._heads(t.transpose(1, 2), "t", (3, 64, 4), cpu)
     with pytest.raises(ValueError, match="expected cuda"):
         paged._heads(t, "t", (3, 4, 64), torch.device("cuda:0"))
-    both = (torch.float32,)
-    paged._output(t.transpose(0, 1), "o", (4, 3, 64), cpu, both)
+    paged._heads(t.transpose(0, 1), "o", (4, 3, 64), cpu, output=True)
+    paged._heads(t[..., 8:], "o", (3, 4, 56), cpu, wide=True)
+    for bad in (t[..., 1:57], torch.as_strided(t, (3, 4, 56), (256, 60, 1))):
+        with pytest.raises(ValueError, match="alignment"):
+            paged._heads(bad, "o", (3, 4, 56), cpu, wide=True)
     for bad in (t[:, :1].expand(3, 4, 64), t[:1].expand(3, 4, 64),
                 torch.as_strided(t, (3, 4, 64), (64, 64, 1))):
         with pytest.raises(ValueError, match="overlap"):
-            paged._output(bad, "o", (3, 4, 64), cpu, both)
+            paged._heads(bad, "o", (3, 4, 64), cpu, output=True)
     f = torch.ones(32, dtype=torch.float64)
-    assert paged._rope(64, cpu, f, None, torch.ones(64), 1e-6, True).rotary_dim == 64
+    k = torch.ones(64)
+    r = lib.nwc_rope.from_buffer_copy(paged._rope(64, cpu, f, None, k, 1e-6, True))
+    assert (r.struct_size, r.rotary_dim, r.interleaved, r.weight_type) == (
+        ctypes.sizeof(r), 64, 1, 1)
+    assert (r.d_freq, r.d_q_weight, r.d_k_weight) == (f.data_ptr(), None, k.data_ptr())
+    assert math.isclose(r.eps, 1e-6, rel_tol=1e-6)
     for bad in (f[:30], torch.ones(64, dtype=torch.float64), f.float(), f[::2], [1.0]):
         with pytest.raises((ValueError, TypeError)):
             paged._rope(64, cpu, bad, None, None, 1e-6, False)
