@@ -146,57 +146,79 @@ constexpr int kBlocks = 5;      // an SM, for prompts: what registers leave with
 
 // What a warp does with one kind of a token's heads.
 struct Turn {
-  bool real;                // else zeros are stored
   bool norm, rotate, interleaved;
   float inv_dim, eps;
   float c[4], s[4];         // of the lane's pairs
   float wa[4], wb[4];       // weights of its quads
 };
 
-// The raw quads of U groups of heads (32 / G heads each): first, first + step, ...
+// Heads come in groups of 32 / G; a warp has groups first, first + step, ....  EXACT:
+// the lanes fill the heads, the groups the number of heads, and whole heads rotate,
+// so that nothing is left to a lane to ask.
+template <int G, bool EXACT>
+struct Groups {
+  int first, step, count, heads;
+  bool on;                  // the lane has elements
+  __device__ __forceinline__ bool has(int g) const {
+    if (EXACT) return g < count;
+    return on && g * (32 / G) + (int)(threadIdx.x & 31) / G < heads;
+  }
+};
+
+// The raw quads of U groups.
 template <typename TIn, int U>
 struct Batch {
   typename RawOf<TIn>::type q[U][2];
 };
-template <typename TIn, int G, bool VEC>
-__device__ __forceinline__ void load_group(typename RawOf<TIn>::type (&q)[2], const TIn* src,
-                                           int64_t src_group, int quad, bool on, int g,
-                                           int heads) {
-  if (on && g * (32 / G) + (int)(threadIdx.x & 31) / G < heads) {
-    q[0] = load_raw(src + g * src_group, VEC);
-    q[1] = load_raw(src + g * src_group + quad, VEC);
-  }
+// src: the lane's first quad in group 0, its second `quad` elements on.
+template <typename TIn, int G, int U, bool VEC, bool EXACT>
+__device__ __forceinline__ void load_groups(Batch<TIn, U>& raw, const Groups<G, EXACT>& of,
+                                            int from, const TIn* src, int64_t group, int quad) {
+  const TIn* p = src + from * group;
+#pragma unroll
+  for (int j = 0; j < U; ++j, p += of.step * group)
+    if (of.has(from + j * of.step)) {
+      raw.q[j][0] = load_raw(p, VEC);
+      raw.q[j][1] = load_raw(p + quad, VEC);
+    }
+}
+template <typename TOut, int G, bool VEC, bool EXACT>
+__device__ __forceinline__ void zero_groups(const Groups<G, EXACT>& of, TOut* dst, int64_t group,
+                                            int quad) {
+  const float none[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int g = of.first; g < of.count; g += of.step)
+    if (of.has(g)) {
+      store4(dst + g * group, VEC, none);
+      store4(dst + g * group + quad, VEC, none);
+    }
 }
 
-// Heads in groups of this warp, U at a time.  src and dst are the lane's first quads
-// in group 0, the second ones `quad` elements on.  The first U groups are in `raw`;
-// where `next` is given, those of the next token replace them as they are used.
-template <typename TIn, typename TOut, int G, int U, bool VEC_IN, bool VEC_OUT>
-__device__ __forceinline__ void turn_heads(const Turn& k, Batch<TIn, U>& raw, const TIn* src,
+// Turns the groups of this warp, U at a time.  The first U are in `raw`; where `next`
+// is given, those of the next token replace them as they are used.  INTER is the
+// pairing where EXACT holds.
+template <typename TIn, typename TOut, int G, int U, bool VEC_IN, bool VEC_OUT, bool EXACT,
+          bool INTER>
+__device__ __forceinline__ void turn_heads(const Turn& k, Batch<TIn, U>& raw,
+                                           const Groups<G, EXACT>& of, const TIn* src,
                                            int64_t src_group, const TIn* next, TOut* dst,
-                                           int64_t dst_group, int quad, bool on, int first,
-                                           int step, int groups, int heads,
-                                           bool place = true) {
-  const int in_group = (int)(threadIdx.x & 31) / G;
+                                           int64_t dst_group, int quad) {
 #pragma unroll 1
-  for (int g0 = first; g0 < groups; g0 += U * step) {
-    if (g0 != first) {
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-        load_group<TIn, G, VEC_IN>(raw.q[j], src, src_group, quad, on, g0 + j * step, heads);
-    }
-    const bool last = g0 + U * step >= groups;
+  for (int g0 = of.first; g0 < of.count; g0 += U * of.step) {
+    if (g0 != of.first)
+      load_groups<TIn, G, U, VEC_IN, EXACT>(raw, of, g0, src, src_group, quad);
+    const bool last = g0 + U * of.step >= of.count;
+    TOut* to = dst + g0 * dst_group;
+    const TIn* ahead = next + of.first * src_group;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       float a[4], b[4];
       widen(raw.q[j][0], a);
       widen(raw.q[j][1], b);
-      if (!k.real) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = b[i] = 0.f;
+      if (next && last && of.has(of.first + j * of.step)) {
+        raw.q[j][0] = load_raw(ahead, VEC_IN);
+        raw.q[j][1] = load_raw(ahead + quad, VEC_IN);
       }
-      if (next && last)
-        load_group<TIn, G, VEC_IN>(raw.q[j], next, src_group, quad, on, first + j * step, heads);
+      ahead += of.step * src_group;
       if (k.norm) {
         float sum = 0.f;
 #pragma unroll
@@ -207,8 +229,8 @@ __device__ __forceinline__ void turn_heads(const Turn& k, Batch<TIn, U>& raw, co
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] *= r * k.wa[i], b[i] *= r * k.wb[i];
       }
-      if (k.rotate) {
-        if (k.interleaved) {
+      if (EXACT || k.rotate) {
+        if (EXACT ? INTER : k.interleaved) {
           // The lane's eight elements are pairs 4u .. 4u + 3 in order.
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -227,19 +249,37 @@ __device__ __forceinline__ void turn_heads(const Turn& k, Batch<TIn, U>& raw, co
           }
         }
       }
-      const int g = g0 + j * step;
-      if (place && on && g * (32 / G) + in_group < heads) {
-        store4(dst + g * dst_group, VEC_OUT, a);
-        store4(dst + g * dst_group + quad, VEC_OUT, b);
+      if (of.has(g0 + j * of.step)) {
+        store4(to, VEC_OUT, a);
+        store4(to + quad, VEC_OUT, b);
       }
+      to += of.step * dst_group;
+    }
+  }
+}
+// V's heads: only rounded.
+template <typename TIn, int G, bool VEC, bool EXACT>
+__device__ __forceinline__ void copy_heads(Batch<TIn, 1>& raw, const Groups<G, EXACT>& of,
+                                           const TIn* src, int64_t src_group, const TIn* next,
+                                           __nv_bfloat16* dst, int64_t dst_group, bool place) {
+  for (int g = of.first; g < of.count; g += of.step) {
+    if (g != of.first) load_groups<TIn, G, 1, VEC, EXACT>(raw, of, g, src, src_group, 4);
+    float a[4], b[4];
+    widen(raw.q[0][0], a);
+    widen(raw.q[0][1], b);
+    if (next && g + of.step >= of.count)
+      load_groups<TIn, G, 1, VEC, EXACT>(raw, of, of.first, next, src_group, 4);
+    if (place && of.has(g)) {
+      store4(dst + g * dst_group, true, a);
+      store4(dst + g * dst_group + 4, true, b);
     }
   }
 }
 
 // G lanes a head; VEC: all quads are aligned for whole loads and stores.  Blocks are
 // token blocks x `splits`, the latter sharing a token's heads.
-template <typename TIn, typename TOut, int G, int U, bool VEC>
-__global__ void __launch_bounds__(kRopeWarps * 32, U == 4 ? kBlocks : 1) rope_kernel(
+template <typename TIn, typename TOut, int G, int U, bool VEC, bool EXACT, bool INTER>
+__global__ void __launch_bounds__(kRopeWarps * 32, U != 4 ? 1 : EXACT ? kBlocks : 4) rope_kernel(
     const __grid_constant__ RopeParams p, int block_tokens, int splits, int groups_q,
     int groups_k) {
   __shared__ float2 turn[kMaxTokens][kMaxDim / 2];   // cosine and sine of each pair
@@ -251,12 +291,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, U == 4 ? kBlocks : 1) rope_ke
   const int tokens = min(block_tokens, p.tokens - token0);
   constexpr int kHeads = 32 / G;
   const int u = lane % G, in_group = lane / G;
-  const bool on = u * 8 < p.dim;
+  const bool on = EXACT || u * 8 < p.dim;
   // The two quads of this lane, in a head that rotates; else 8 u and the next.
   const int half = p.rotary / 2;
   Turn k;
-  k.rotate = u * 8 < p.rotary;
-  k.interleaved = p.interleaved != 0;
+  k.rotate = EXACT || u * 8 < p.rotary;
+  k.interleaved = EXACT ? INTER : p.interleaved != 0;
   k.inv_dim = 1.f / (float)p.dim;
   k.eps = p.eps;
   const bool apart = k.rotate && !k.interleaved;
@@ -265,6 +305,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32, U == 4 ? kBlocks : 1) rope_ke
   // Few k and v heads: of the warps behind the last with q, and with k, first.
   const int first_k = (first + step - groups_q % step) % step;
   const int first_v = (first_k + step - groups_k % step) % step;
+  const Groups<G, EXACT> of_q{first, step, groups_q, p.heads, on};
+  const Groups<G, EXACT> of_k{first_k, step, groups_k, p.kv_heads, on};
+  const Groups<G, EXACT> of_v{first_v, step, groups_k, p.kv_heads, on};
   const int64_t q_group = kHeads * p.q.head_stride, k_group = kHeads * p.k.head_stride,
                 v_group = kHeads * p.v.head_stride;
   const TIn* q_src = static_cast<const TIn*>(p.q.data) + (int64_t)token0 * p.q.token_stride +
@@ -278,15 +321,18 @@ __global__ void __launch_bounds__(kRopeWarps * 32, U == 4 ? kBlocks : 1) rope_ke
   // The first token's heads are on their way while the places and angles are found.
   Batch<TIn, U> raw_q = {};
   Batch<TIn, 1> raw_k = {}, raw_v = {};
-  if (p.q.data) {
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-      load_group<TIn, G, VEC>(raw_q.q[j], q_src, q_group, quad, on, first + j * step, p.heads);
-  }
-  if (p.k.data)
-    load_group<TIn, G, VEC>(raw_k.q[0], k_src, k_group, quad, on, first_k, p.kv_heads);
-  if (p.append)
-    load_group<TIn, G, VEC>(raw_v.q[0], v_src, v_group, 4, on, first_v, p.kv_heads);
+  auto bring = [&](int t) {
+    if (p.q.data)
+      load_groups<TIn, G, U, VEC, EXACT>(raw_q, of_q, first, q_src + t * p.q.token_stride,
+                                         q_group, quad);
+    if (p.k.data)
+      load_groups<TIn, G, 1, VEC, EXACT>(raw_k, of_k, first_k, k_src + t * p.k.token_stride,
+                                         k_group, quad);
+    if (p.append)
+      load_groups<TIn, G, 1, VEC, EXACT>(raw_v, of_v, first_v, v_src + t * p.v.token_stride,
+                                         v_group, 4);
+  };
+  bring(0);
   for (int t = warp; t < tokens; t += kRopeWarps) {
     Place at;
     if (p.append) {
@@ -331,24 +377,29 @@ __global__ void __launch_bounds__(kRopeWarps * 32, U == 4 ? kBlocks : 1) rope_ke
   for (int t = 0; t < tokens; ++t) {
     const Place at = places[t];
     const int64_t token = token0 + t;
-    k.real = at.real;
+    const bool more = t + 1 < tokens && places[t + 1].real;
+    TOut* q_dst = static_cast<TOut*>(p.q_out.data) + token * p.q_out.token_stride +
+                  in_group * p.q_out.head_stride + oa;
+    if (!at.real) {   // padding
+      if (p.q.data)
+        zero_groups<TOut, G, VEC, EXACT>(of_q, q_dst, kHeads * p.q_out.head_stride, quad);
+      if (more) bring(t + 1);
+      continue;
+    }
     if (k.rotate) {
       const float4 lo = *reinterpret_cast<const float4*>(&turn[t][4 * u]);
       const float4 hi = *reinterpret_cast<const float4*>(&turn[t][4 * u + 2]);
       k.c[0] = lo.x, k.c[1] = lo.z, k.c[2] = hi.x, k.c[3] = hi.z;
       k.s[0] = lo.y, k.s[1] = lo.w, k.s[2] = hi.y, k.s[3] = hi.w;
     }
-    const bool more = t + 1 < tokens && places[t + 1].real;
     if (p.q.data) {
       k.norm = p.q_weight != nullptr;
 #pragma unroll
       for (int i = 0; i < 4; ++i) k.wa[i] = w[0][0][i], k.wb[i] = w[0][1][i];
       const TIn* src = q_src + t * p.q.token_stride;
-      turn_heads<TIn, TOut, G, U, VEC, VEC>(
-          k, raw_q, src, q_group, more ? src + p.q.token_stride : nullptr,
-          static_cast<TOut*>(p.q_out.data) + token * p.q_out.token_stride +
-              in_group * p.q_out.head_stride + oa,
-          kHeads * p.q_out.head_stride, quad, on, first, step, groups_q, p.heads);
+      turn_heads<TIn, TOut, G, U, VEC, VEC, EXACT, INTER>(
+          k, raw_q, of_q, src, q_group, more ? src + p.q.token_stride : nullptr, q_dst,
+          kHeads * p.q_out.head_stride, quad);
     }
     if (!p.k.data) continue;
     k.norm = p.k_weight != nullptr;
@@ -357,31 +408,32 @@ __global__ void __launch_bounds__(kRopeWarps * 32, U == 4 ? kBlocks : 1) rope_ke
     const TIn* src = k_src + t * p.k.token_stride;
     const TIn* next = more ? src + p.k.token_stride : nullptr;
     if (!p.append) {
-      turn_heads<TIn, TOut, G, 1, VEC, VEC>(
-          k, raw_k, src, k_group, next,
+      turn_heads<TIn, TOut, G, 1, VEC, VEC, EXACT, INTER>(
+          k, raw_k, of_k, src, k_group, next,
           static_cast<TOut*>(p.k_out.data) + token * p.k_out.token_stride +
               in_group * p.k_out.head_stride + oa,
-          kHeads * p.k_out.head_stride, quad, on, first_k, step, groups_k, p.kv_heads);
+          kHeads * p.k_out.head_stride, quad);
       continue;
     }
-    // Pages are 16-byte aligned with strides of 8 elements (checked on the host).  A
-    // row without a place still brings the next one's heads.
+    // Pages are 16-byte aligned with strides of 8 elements (checked on the host).
     const CacheView& cv = p.cache;
     const bool place = at.slot_page >= 0;
-    const int64_t page = place ? at.slot_page : 0;
-    turn_heads<TIn, __nv_bfloat16, G, 1, VEC, true>(
-        k, raw_k, src, k_group, next,
-        reinterpret_cast<__nv_bfloat16*>(cv.k) + page * cv.k_page + at.slot * cv.k_token +
-            in_group * cv.k_head + oa,
-        kHeads * cv.k_head, quad, on, first_k, step, groups_k, p.kv_heads, place);
-    Turn plain = k;
-    plain.norm = plain.rotate = false;
-    src = v_src + t * p.v.token_stride;
-    turn_heads<TIn, __nv_bfloat16, G, 1, VEC, true>(
-        plain, raw_v, src, v_group, more ? src + p.v.token_stride : nullptr,
-        reinterpret_cast<__nv_bfloat16*>(cv.v) + page * cv.v_page + at.slot * cv.v_token +
-            in_group * cv.v_head + 8 * u,
-        kHeads * cv.v_head, 4, on, first_v, step, groups_k, p.kv_heads, place);
+    const TIn* v = v_src + t * p.v.token_stride;
+    const TIn* next_v = more ? v + p.v.token_stride : nullptr;
+    if (place) {
+      turn_heads<TIn, __nv_bfloat16, G, 1, VEC, true, EXACT, INTER>(
+          k, raw_k, of_k, src, k_group, next,
+          reinterpret_cast<__nv_bfloat16*>(cv.k) + at.slot_page * cv.k_page +
+              at.slot * cv.k_token + in_group * cv.k_head + oa,
+          kHeads * cv.k_head, quad);
+    } else if (next) {
+      load_groups<TIn, G, 1, VEC, EXACT>(raw_k, of_k, first_k, next, k_group, quad);
+    }
+    copy_heads<TIn, G, VEC, EXACT>(
+        raw_v, of_v, v, v_group, next_v,
+        reinterpret_cast<__nv_bfloat16*>(cv.v) + (place ? at.slot_page : 0) * cv.v_page +
+            at.slot * cv.v_token + in_group * cv.v_head + 8 * u,
+        kHeads * cv.v_head, place);
   }
 }
 
@@ -414,10 +466,16 @@ cudaError_t launch_t(const RopeParams& p, int sm_count, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // Four head groups of q in flight a warp where it has as many.
-  return large ? cudaLaunchKernelEx(&cfg, rope_kernel<TIn, TOut, G, 4, VEC>, p, block_tokens,
-                                    splits, groups_q, groups_k)
-               : cudaLaunchKernelEx(&cfg, rope_kernel<TIn, TOut, G, 1, VEC>, p, block_tokens,
-                                    splits, groups_q, groups_k);
+  auto run = [&](auto kernel) {
+    return cudaLaunchKernelEx(&cfg, kernel, p, block_tokens, splits, groups_q, groups_k);
+  };
+  if (!large) return run(rope_kernel<TIn, TOut, G, 1, VEC, false, false>);
+  const bool exact = VEC && p.dim == 8 * G && p.rotary == p.dim &&
+                     (!p.q.data || p.heads % kHeads == 0) &&
+                     (!p.k.data || p.kv_heads % kHeads == 0);
+  if (!exact) return run(rope_kernel<TIn, TOut, G, 4, VEC, false, false>);
+  return p.interleaved ? run(rope_kernel<TIn, TOut, G, 4, true, true, true>)
+                       : run(rope_kernel<TIn, TOut, G, 4, true, true, false>);
 }
 
 template <typename TIn, typename TOut, bool VEC>
