@@ -319,7 +319,7 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 }
 
 // Where this CTA's share of the axis starts: the producer warp sums the segments,
-// four consecutive ones a lane, for the totals, then for the segment in which the
+// up to four consecutive ones a lane, for the totals, then for the segment in which the
 // share starts (from registers where there are up to 128).  Of an item's CTAs none
 // may be without a tile (the join counts on it), so a share is at least as long as
 // the widest gap between two tiles' starts, the most that a tile costs plus a lead:
@@ -328,25 +328,31 @@ __device__ __forceinline__ Walk share_out(const AttentionParams& p, bool dry) {
   const BatchView& b = p.batch;
   const int segments = b.groups + b.sequences;
   const int lane = threadIdx.x & 31;
+  const int per = min((segments + 31) / 32, 4);   // segments of a lane
   const int chunks = (segments + 127) / 128;
   Segment g[4];
   auto take = [&](int s0) {
     Raw raw[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) raw[j] = raw_segment(b, s0 + j, s0 + j < segments, dry);
+    for (int j = 0; j < 4; ++j)
+      if (j < per) raw[j] = raw_segment(b, s0 + j, s0 + j < segments, dry);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      g[j] = segment_of(p, s0 + j, raw[j]);
-      if (s0 + j >= segments) g[j].tiles = g[j].items = 0;
+      if (j < per) g[j] = segment_of(p, s0 + j, raw[j]);
+      if (j >= per || s0 + j >= segments) {
+        g[j].tiles = g[j].items = g[j].cost = g[j].lead = 0;
+        g[j].kind = kFew;
+      }
     }
   };
   int64_t tiles = 0, cost = 0;
   int of_kind[3] = {0, 0, 0};   // items of each kind
 #pragma unroll 1
   for (int t = 0; t < chunks; ++t) {
-    take(t * 128 + 4 * lane);
+    take(t * 128 + per * lane);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (j >= per) break;
       const int64_t all = (int64_t)g[j].tiles * g[j].items;
       tiles += all;
       cost += all * cost_of(g[j].kind, p.dim == 128);
@@ -379,12 +385,14 @@ __device__ __forceinline__ Walk share_out(const AttentionParams& p, bool dry) {
   int32_t run_items = 0;
 #pragma unroll 1
   for (int t = 0; t < chunks && run <= walk.from; ++t) {
-    const int s0 = t * 128 + 4 * lane;
+    const int s0 = t * 128 + per * lane;
     if (chunks > 1) take(s0);
     int64_t span[4], sum = 0;
     int32_t n = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      span[j] = 0;
+      if (j >= per) break;
       price(p, g[j], walk.cap);
       span[j] = item_span(g[j]) * g[j].items;
       sum += span[j];
@@ -407,6 +415,7 @@ __device__ __forceinline__ Walk share_out(const AttentionParams& p, bool dry) {
     int32_t first = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (j >= per) break;
       if (at <= walk.from && walk.from < at + span[j]) mine = s0 + j, start = at, first = item0;
       at += span[j];
       item0 += g[j].items;
