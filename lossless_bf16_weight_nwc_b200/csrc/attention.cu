@@ -579,6 +579,7 @@ struct Unit {
   uint32_t tile;   // of the CTA
   bool first;      // the team's first of a part
   bool last;       // the team's last of a part
+  bool both;       // the other team uses the tile, too
 };
 struct Units {
   uint32_t tile = 0, team = 0, k = 0;
@@ -613,6 +614,7 @@ struct Units {
     begun |= 1 << team;
     --left;
     u.last = left < 2;
+    u.both = both;
     if (!both || (left & 1) == 0) ++tile;
     team ^= 1;
     return true;
@@ -620,9 +622,11 @@ struct Units {
 };
 
 // Issues every product of the CTA (a whole warp, its first lane in effect).  A
-// commit costs the issuer about as much as two products, so there is one a unit:
-// it follows a team's P V and the S of its next unit, and the team passes the
-// tiles it has then done with back to the producer.
+// commit costs the issuer about as much as two products, so tiles that both teams use
+// get one a unit: it follows a team's P V and the S of its next unit, and the teams
+// pass the tiles they have then done with back to the producer.  Where a tile has one
+// user memory is the bound, and V goes back by a commit of its own (so that two thirds
+// of the ring are on their way instead of two fifths).
 template <int DIM>
 __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* bars,
                                const Ctl& ctl) {
@@ -661,6 +665,10 @@ __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* ba
       umma_bf16_ts_by(leader, tmem + 256u + w * 128u, tmem + w * 128u + 8u * k,
                       b + ((uint32_t)k * 2048u >> 4), id_o, !u.first || k > 0);
     if (u.last) umma_commit_by(leader, &bars->ofull[w]);
+    if (!u.both) {   // alone with V: it goes back as soon as it has been read
+      if (leader) mbar_arrive_n(&bars->empty[slot], 7);
+      umma_commit_by(leader, &bars->empty[slot]);
+    }
     return true;
   };
 
@@ -998,7 +1006,6 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
     const int team_rows = min(part.rows - from, kTeamRows);
     const int first = both ? 0 : (int)((uses ^ w) & 1u);         // the team's first tile
     const int step = both ? 1 : 2;
-    const int last = first + (part.n - 1 - first) / step * step;  // (when first < part.n)
     const bool zeroes = !both || w == (uses & 1u);               // the tile's first user
     const bool begins = first < part.n;
     // This thread's row; a team without a tile only leaves word that it has nothing.
@@ -1036,11 +1043,10 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
       const int t0 = (part.tile0 + t) * kKvTile;
       if (!__all_sync(kAll, wait(&bars->sfull[w], turn & 1u, ctl))) return;
       tc_fence_after();
-      if (r == 0) {   // S is there: K has been read, and the V of the unit before
+      if (r == 0) {   // S is there: K has been read, and a shared V of the unit before
         mbar_arrive_n(&bars->empty[2 * (tiles + (uint32_t)t) % L::kRing], both ? 4 : 8);
-        if (t != first)
-          mbar_arrive_n(&bars->empty[(2 * (tiles + (uint32_t)(t - step)) + 1) % L::kRing],
-                        both ? 4 : 8);
+        if (both && t != first)
+          mbar_arrive_n(&bars->empty[(2 * (tiles + (uint32_t)(t - 1)) + 1) % L::kRing], 4);
       }
       if (warp_live) {
         // Rows that are not there need no mask: nothing of theirs is read.
@@ -1148,9 +1154,8 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
     if (begins) {
       if (!__all_sync(kAll, wait(&bars->ofull[w], done++ & 1u, ctl))) return;
       tc_fence_after();
-      if (r == 0)
-        mbar_arrive_n(&bars->empty[(2 * (tiles + (uint32_t)last) + 1) % L::kRing],
-                      both ? 4 : 8);
+      if (both && r == 0)
+        mbar_arrive_n(&bars->empty[(2 * (tiles + (uint32_t)part.n) - 1) % L::kRing], 4);
       if (warp_live) {
         // Rows of a lane each become rows of a warp through the Q buffer (pieces of
         // 16 bytes, spread over the banks): a lane's own row of 512 bytes stored
