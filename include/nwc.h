@@ -417,7 +417,8 @@ typedef struct {
  * Lengths below zero count as zero.  A token beyond its table (or the 2^30th), or
  * on a page outside [0, pages), sets error bit 4: it is not appended, and
  * attention sees no token past the table and zeros for the page.
- * sequences x new_tokens <= 2^24; groups <= sequences. */
+ * sequences x new_tokens <= 2^24; groups <= sequences.  A table of width 0 holds no
+ * page (and may be NULL). */
 typedef struct {
   uint32_t struct_size;
   int32_t sequences, new_tokens;

@@ -74,15 +74,15 @@ bool good_batch(const nwc_kv_batch* b) {
     return false;
   if (b->groups < 0 || b->groups > b->sequences) return false;
   if (b->sequences == 0) return true;
-  if (b->table_width < 1 || !b->d_block_table || !b->d_seq_lens || b->table_stride < 0 ||
-      b->table_stride > kMaxStride)
+  if (b->table_width < 0 || (b->table_width && !b->d_block_table) || !b->d_seq_lens ||
+      b->table_stride < 0 || b->table_stride > kMaxStride)
     return false;
   if (!aligned_to(b->d_block_table, 4) || !aligned_to(b->d_seq_lens, 4) ||
       !aligned_to(b->d_q_lens, 4))
     return false;
   if (b->groups == 0) return true;
-  return b->d_group_start && b->d_prefix_table && b->d_prefix_lens && b->prefix_width >= 1 &&
-         b->prefix_stride >= 0 && b->prefix_stride <= kMaxStride &&
+  return b->d_group_start && b->d_prefix_lens && b->prefix_width >= 0 &&
+         (b->d_prefix_table || !b->prefix_width) && b->prefix_stride >= 0 && b->prefix_stride <= kMaxStride &&
          aligned_to(b->d_group_start, 4) && aligned_to(b->d_prefix_table, 4) &&
          aligned_to(b->d_prefix_lens, 4);
 }

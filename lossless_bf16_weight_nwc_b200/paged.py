@@ -292,8 +292,8 @@ class PagedBatch:
             raise TypeError(f"{what}: expected an int32 tensor [rows, width]")
         if t.device != self.device:
             raise ValueError(f"{what}: on {t.device}, expected {self.device}")
-        if t.shape[0] and (t.shape[1] < 1 or (t.stride(1) != 1 and t.shape[1] > 1)):
-            raise ValueError(f"{what}: its rows must be contiguous and not empty")
+        if t.stride(1) != 1 and t.shape[1] > 1:
+            raise ValueError(f"{what}: its rows must be contiguous")
         return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.shape[1]
 
     def _view(self, rows: int):

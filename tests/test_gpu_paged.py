@@ -242,6 +242,33 @@ def test_append(paged, lens, chunk, q_lens, kw, tin, inter):
     assert c.kv.device_error() == (0, 0)
 
 
+def test_tables_of_no_width(paged):
+    """A prefix table without columns, for prefixes of no tokens; own tables without."""
+    c = Case(paged, 17, [9, 30], poison=False)
+    far = torch.zeros((1, 0), dtype=torch.int32, device="cuda")
+    batch = paged.PagedBatch(c.table, ints(c.lens), None, far, ints([0]), ints([0, 2]))
+    q, k, v = (randn(c.g, 2, n, 64).bfloat16() for n in (4, 2, 2))
+    c.kv.append(batch, k, v)
+    assert torch.equal(c.v[c.table[0, 0], 8], v[0])
+    got, lse = c.kv.attend(batch, q, return_lse=True)
+    c.check(q, got, lse)
+    none = paged.PagedBatch(far.expand(2, 0), ints([0, 0]))
+    assert not c.kv.attend(none, q).any() and c.kv.device_error() == (0, 0)
+    k0 = c.k.clone()
+    c.kv.append(paged.PagedBatch(far.expand(2, 0), ints([1, 1])), k, v)
+    assert torch.equal(bits(c.k), bits(k0)) and c.kv.device_error() == (1, 4)
+
+
+def test_empty_batches(paged):
+    c = Case(paged, 18, [9], poison=False)
+    table = torch.zeros((0, 3), dtype=torch.int32, device="cuda")
+    none = paged.PagedBatch(table, ints([]))
+    q, k = (torch.zeros((0, n, 64), dtype=torch.bfloat16, device="cuda") for n in (4, 2))
+    assert c.kv.append(none, k, k, q=q).shape == (0, 4, 64)
+    o, lse = c.kv.attend(none, q, return_lse=True)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
 def test_append_large_batches_and_heads(paged):
     """More tokens than fill the device, heads that do not fill a warp's group."""
     for seqs, h, hk, dim in ((1500, 5, 1, 64), (1300, 3, 3, 80), (1250, 2, 1, 256)):

@@ -82,12 +82,13 @@ CACHE_BAD = [dict(page_size=12), dict(page_size=4), dict(page_size=1 << 21), dic
              dict(struct_size=0)]
 BATCH_BAD = [dict(sequences=-1), dict(new_tokens=0), dict(sequences=1 << 20, new_tokens=1 << 10),
              dict(groups=-1), dict(groups=1), dict(struct_size=4),
-             dict(sequences=2, table_width=0), dict(sequences=2, d_block_table=None),
+             dict(sequences=2, table_width=-1), dict(sequences=2, d_block_table=None),
              dict(sequences=2, d_seq_lens=None), dict(sequences=2, d_seq_lens=0x2002),
              dict(sequences=2, table_stride=-1), dict(sequences=2, d_q_lens=0x2001),
              dict(sequences=2, groups=1, prefix_width=1, d_prefix_table=0x100, d_prefix_lens=0x100),
-             dict(sequences=2, groups=1, prefix_width=0, d_prefix_table=0x100, d_prefix_lens=0x100,
-                  d_group_start=0x100)]
+             dict(sequences=2, groups=1, prefix_width=-1, d_prefix_table=0x100, d_prefix_lens=0x100,
+                  d_group_start=0x100),
+             dict(sequences=2, groups=1, prefix_width=1, d_prefix_lens=0x100, d_group_start=0x100)]
 
 
 def test_append_arguments(lib):
