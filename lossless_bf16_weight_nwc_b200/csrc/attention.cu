@@ -23,8 +23,8 @@
 // A second kernel joins the parts' results in a fixed order.
 //
 // B200, 32 query heads over 8 key heads of 128: 64 sequences of 100 to 1900 own tokens
-// behind 32768 shared ones take 88 us (406 MB, 4.6 TB/s, 0.71 of a copy's rate); 64
-// without a prefix 55 us (0.71); 64 rows of one sequence over 16400 tokens 39 us (444
+// behind 32768 shared ones take 89 us (406 MB, 4.6 TB/s, 0.70 of a copy's rate); 64
+// without a prefix 55 us (0.71); 64 rows of one sequence over 16400 tokens 40 us (430
 // TFLOP/s): 13 us of a start, Q and results around 7 tiles a CTA; one row over 1003
 // tokens 12 us, of which 4 in the second kernel.
 #include <cuda_bf16.h>
@@ -744,8 +744,9 @@ __device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo) + 0x8000u, __float_as_uint(hi) + 0x8000u, 0x7632);
 }
 
-// A part of a segment of at most kFewRows rows.  128 rows would keep the tensor
-// cores busy with padding for longer than memory takes to bring the tile, so each
+// A part of a segment of at most kFewRows rows (what the registers of G = 2 hold).  128
+// rows would keep the tensor cores and a team's chain busy with padding (3,800 cycles a
+// tile of 64 KiB against 1,600 here; memory's share of one is 2,700), so each
 // of the eight softmax warps takes one head's 16 tokens of every tile and
 // multiplies them in registers (m16n8k16: S^T = K Q^T with the tokens as M, O^T +=
 // V^T P^T with the elements as M, G groups of eight rows as N), on its own until
