@@ -48,7 +48,7 @@ constexpr int kThreads = 10 * 32;
 constexpr int kMaxRing = 12;
 constexpr int kQueue = 5;                // parts announced ahead
 constexpr uint32_t kRingBytes = 163840;  // K and V tiles: 5 of dim 128, 10 of dim 64
-constexpr uint32_t kBarBytes = 3072;
+constexpr uint32_t kBarBytes = 3 * 1024;
 constexpr float kLazy = 8.f;             // growth of the maximum (log2) that rescales O
 
 template <int DIM>
@@ -1330,7 +1330,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   far.n = own.n = 0;
   const int fresh = fresh_of(b, seq);
   if (i < fresh) {
-    if (b.lens[seq] > 0)
+    // (Tokens that no table holds have no parts: what the workspace says is then old.)
+    if (b.lens[seq] > 0 && b.table_width > 0)
       own = side_of(p, false, p.seq_rows, in_seq, kvh, (int64_t)seq * p.ws.own_items);
     for (int g0 = 0; g0 < b.groups; g0 += 32) {
       const int g = g0 + lane;
@@ -1347,7 +1348,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         first = max(__shfl_sync(kAll, first, from), 0);
         end = min(__shfl_sync(kAll, end, from), b.sequences);
         item = __shfl_sync(kAll, item, from);
-        if (__shfl_sync(kAll, len, from) > 0)
+        if (__shfl_sync(kAll, len, from) > 0 && b.prefix_width > 0)
           far = side_of(p, true, (end - first) * p.seq_rows, (seq - first) * p.seq_rows + in_seq,
                         kvh, item);
         break;

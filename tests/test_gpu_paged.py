@@ -495,6 +495,39 @@ def test_attend_bounded_waits(paged):
     c.check(q, got, lse)
 
 
+def test_attend_tables_without_columns_after_others(paged):
+    """Lengths that no table holds leave nothing to see, whatever an earlier call of
+    the same shape left in the workspace."""
+    from lossless_bf16_weight_nwc_b200 import _lib
+    c = Case(paged, 19, [40, 30], prefix=[50], starts=[0, 2], poison=False)
+    q = randn(c.g, 2, 4, 64).bfloat16()
+    none = torch.zeros((2, 0), dtype=torch.int32, device="cuda")
+    shared = (ints(c.prefix), ints(c.starts))
+    empty = paged.PagedBatch(none, ints(c.lens), None, none[:1], *shared)
+    own = paged.PagedBatch(c.table, ints(c.lens), None, none[:1], *shared)
+    need = [_lib.nwc_kv_attention_workspace(c.kv._view, _lib.nwc_kv_batch.from_address(b._view(2)), 4)
+            for b in (c.batch, empty)]
+    assert need[0] == need[1]
+    ws = torch.zeros(need[0], dtype=torch.uint8, device="cuda")
+
+    def attend(batch):
+        out, lse = torch.full_like(q, 7.0), torch.full((2, 4), 7.0, device="cuda")
+        view = [_lib.nwc_heads.from_buffer_copy(paged._heads(t, "t", t.shape, t.device))
+                for t in (q, out)]
+        _lib.nwc_kv_attention(c.kv._view, _lib.nwc_kv_batch.from_address(batch._view(2)), view[0],
+                              4, 1 / 8, view[1], lse, ws, need[0])
+        return out, lse
+
+    c.check(q, *attend(c.batch))
+    out, lse = attend(empty)
+    assert not out.any() and bool((lse == -math.inf).all())
+    assert c.kv.device_error() == (1, 4)
+    attend(c.batch)
+    want, bound, _, _ = ref.attention(q, c.k, c.v, c.table, c.lens, None, None, None, None, 1 / 8)
+    assert ref.close(attend(own)[0], want, bound, torch.bfloat16)
+    assert c.kv.device_error() == (1, 4)
+
+
 def test_attend_unordered_groups(paged):
     """Group starts that are not ascending or point outside: some answer, nothing
     written out of bounds, and the rows outside such groups are right."""
