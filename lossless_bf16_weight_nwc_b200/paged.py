@@ -65,8 +65,8 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, device="cuda",
 def _no_grad(*tensors) -> None:
     if torch.is_grad_enabled():
         for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError("an input requires a gradient, which these kernels do not "
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError("a tensor requires a gradient, which these kernels do not "
                                  "give; call under torch.no_grad()")
 
 
@@ -203,7 +203,7 @@ def qk_norm_rope(q, k, positions, freq=None, q_weight=None, k_weight=None, eps: 
     themselves) holds."""
     first = q if q is not None else k
     device = _cuda(first, "q" if q is not None else "k")
-    _no_grad(q, k, q_weight, k_weight)
+    _no_grad(q, k, freq, q_weight, k_weight, *(out or ()))
     if first.dim() != 3:
         raise ValueError("q, k: expected [tokens, heads, dim]")
     tokens, heads, dim = first.shape
@@ -382,7 +382,7 @@ class PagedKV:
         seq_lens counts the new tokens already.  Padding rows are not appended,
         their q is zero."""
         rows, view = self._rows(batch, k, "k")
-        _no_grad(q, k, v, q_weight, k_weight)
+        _no_grad(q, k, v, freq, q_weight, k_weight, q_out)
         device = self.device
         shape = (rows, self.kv_heads, self.dim)
         kh = _heads(k, "k", shape, device)
@@ -419,7 +419,7 @@ class PagedKV:
         with return_lse also FP32 [rows, heads], the logarithm of the sum of
         exponentials.  A row that sees nothing, and a padding row, is zero (-inf)."""
         rows, view = self._rows(batch, q, "q")
-        _no_grad(q)
+        _no_grad(q, out)
         if self.dim not in (64, 128):
             raise ValueError(f"dim {self.dim}: attention takes heads of 64 or 128")
         heads = q.shape[1]
@@ -478,6 +478,7 @@ class AttentionBlock:
 
     def step(self, x, batch: PagedBatch):
         """x BF16 [rows, wqkv.cols], 1 to 64 rows, a sequence's rows together."""
+        _no_grad(x)
         dim = self.cache.dim
         q, k, v = (t.unflatten(-1, (-1, dim)) for t in self.wqkv.split(self.wqkv.gemv(x)))
         q = self.cache.append(batch, k, v, q=q, freq=self.freq, q_weight=self.q_weight,

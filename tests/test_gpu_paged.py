@@ -528,6 +528,38 @@ def test_attend_tables_without_columns_after_others(paged):
     assert c.kv.device_error() == (1, 4)
 
 
+def test_gradients_are_refused_everywhere(paged):
+    """Every tensor of a call that requires a gradient, results' own included."""
+    from lossless_bf16_weight_nwc_b200 import _lib, synth
+    c = Case(paged, 20, [9, 30], poison=False)
+    q, k, v = (randn(c.g, 2, n, 64).bfloat16() for n in (4, 2, 2))
+    freq, at, w = paged.rope_frequencies(64), ints([1, 2]), torch.ones(64, device="cuda")
+    eye = [synth.matrix(synth.MatrixSpec("w", r, 256, "normal", 0.06, 0), 1)
+           for r in (256, 128, 128, 256)]
+    block = paged.AttentionBlock(_lib.CompressedMatrix.compress_fused(eye[:3]),
+                                 _lib.CompressedMatrix.compress(eye[3]), c.kv, freq)
+    x = randn(c.g, 2, 256).bfloat16()
+    calls = [(lambda t: paged.qk_norm_rope(t, k, at, freq), q),
+             (lambda t: paged.qk_norm_rope(q, k, at, t), freq),
+             (lambda t: paged.qk_norm_rope(q, k, at, freq, t), w),
+             (lambda t: paged.qk_norm_rope(q, None, at, freq, out=(t, None)), q),
+             (lambda t: c.kv.append(c.batch, t, v), k), (lambda t: c.kv.append(c.batch, k, t), v),
+             (lambda t: c.kv.append(c.batch, k, v, freq=t), freq),
+             (lambda t: c.kv.append(c.batch, k, v, q=q, q_out=t), q),
+             (lambda t: c.kv.attend(c.batch, t), q),
+             (lambda t: c.kv.attend(c.batch, q, out=t), q),
+             (lambda t: block.step(t, c.batch), x)]
+    k0, v0 = bits(c.k), bits(c.v)
+    for call, t in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call(t.clone().requires_grad_())
+    assert torch.equal(bits(c.k), k0) and torch.equal(bits(c.v), v0)
+    with torch.no_grad():
+        for call, t in calls:
+            call(t.clone().requires_grad_())
+    assert c.kv.device_error() == (0, 0)
+
+
 def test_attend_unordered_groups(paged):
     """Group starts that are not ascending or point outside: some answer, nothing
     written out of bounds, and the rows outside such groups are right."""
