@@ -459,7 +459,7 @@ nwc_status nwc_kv_attention_workspace(const nwc_kv_cache* cache, const nwc_kv_ba
  * tokens up to and including itself.  A prefix is read once for all the rows
  * that share it.
  *   q, out: [rows][heads][dim], BF16, 16-byte aligned with strides of 8
- *     elements.  heads: a multiple of kv_heads; rows x heads / kv_heads <= 2^30.
+ *     elements; out may be q.  heads: a multiple of kv_heads; rows x heads / kv_heads <= 2^30.
  *     dim: 64 or 128 (others: UNSUPPORTED).
  *   d_lse (or NULL): FP32 [rows][heads], the natural logarithm of the sum of
  *     exp(scale q . K) over the row's tokens.
@@ -469,9 +469,8 @@ nwc_status nwc_kv_attention_workspace(const nwc_kv_cache* cache, const nwc_kv_ba
  * A row that sees no token, and a padding row, is zero with d_lse -infinity.
  * Scores, sums and the running maximum are FP32; a probability is rounded to
  * BF16 before it multiplies V.  Memory behind a sequence's or a prefix's last
- * token is not used, whatever it holds; but a V that is not finite, of a call's new
- * token, may reach the rows before it in the same call.  The result is the same bit
- * pattern on every run.
+ * token, and tokens that a row does not see, play no part in it, whatever they hold.
+ * The result is the same bit pattern on every run.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA (launch). */
 nwc_status nwc_kv_attention(const nwc_kv_cache* cache, const nwc_kv_batch* batch,
                             const nwc_heads* q, int32_t heads, float scale,

@@ -24,7 +24,7 @@
 //
 // B200, 32 query heads over 8 key heads of 128: 64 sequences of 100 to 1900 own tokens
 // behind 32768 shared ones take 89 us (406 MB, 4.6 TB/s, 0.70 of a copy's rate); 64
-// without a prefix 55 us (0.71); 64 rows of one sequence over 16400 tokens 40 us (430
+// without a prefix 55 us (0.71); 64 rows of one sequence over 16400 tokens 41 us (420
 // TFLOP/s): 13 us of a start, Q and results around 7 tiles a CTA; one row over 1003
 // tokens 12 us, of which 4 in the second kernel.
 #include <cuda_bf16.h>
@@ -979,6 +979,12 @@ __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* sm
   return __all_sync(kAll, wait(&bars->team[w], (*meets)++ & 1u, ctl));
 }
 
+// Scores are in units of log2; a scale of zero is replaced by one that leaves every
+// finite score at zero (so that masked scores of -inf stay what they are).
+__device__ __forceinline__ float score_unit(float scale) {
+  return fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-38f);
+}
+
 // A softmax team: thread r has row r of the team's rows.
 template <int DIM>
 __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars,
@@ -988,10 +994,8 @@ __device__ void softmax_team(const AttentionParams& p, uint8_t* smem, Bars* bars
   const uint32_t lane_base = (uint32_t)(r & ~31) << 16;
   const uint32_t ts = bars->tmem + w * 128u + lane_base;         // S and P
   const uint32_t to = bars->tmem + 256u + w * 128u + lane_base;  // O
-  // Scores in units of log2; a negative scale turns Q's sign, which is exact, and
-  // one of zero is replaced by one that leaves every finite score at zero (so that
-  // masked scores of -inf stay what they are).
-  const float c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-38f);
+  // (A negative scale turns Q's sign, which is exact.)
+  const float c = score_unit(p.scale);
   const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
   uint32_t turn = 0;       // this team's uses of tiles so far
   uint32_t done = 0;       // and its parts with at least one
@@ -1308,10 +1312,37 @@ __device__ __forceinline__ Side side_of(const AttentionParams& p, bool far, int 
   return d;
 }
 
+// Weighted values of a segment's first `limit` tokens for one row, by a warp token by
+// token, E elements a lane, with the row's maximum known: for rows where a V that they do
+// not see spoilt the products (zero times infinity is not zero).
+template <int DIM>
+__device__ __noinline__ void add_seen(const AttentionParams& p, const int32_t* table, int limit,
+                                      int kvh, const uint16_t (&q)[DIM / 32], float top,
+                                      float* acc) {
+  constexpr int E = DIM / 32;
+  const CacheView& cv = p.cache;
+  const int lane = threadIdx.x & 31, mask = (1 << cv.page_shift) - 1;
+  const float c = copysignf(score_unit(p.scale), p.scale);
+  float qe[E];
+  for (int e = 0; e < E; ++e) qe[e] = __uint_as_float((uint32_t)q[e] << 16);
+  for (int j = 0; j < limit; ++j) {
+    const int64_t page = table[j >> cv.page_shift];
+    if (page < 0 || page >= cv.pages) continue;   // its V counts as zeros
+    const uint16_t* k = cv.k + page * cv.k_page + (j & mask) * cv.k_token + kvh * cv.k_head;
+    const uint16_t* v = cv.v + page * cv.v_page + (j & mask) * cv.v_token + kvh * cv.v_head;
+    float s = 0.f;
+    for (int e = 0; e < E; ++e) s += qe[e] * __uint_as_float((uint32_t)k[lane * E + e] << 16);
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kAll, s, d);
+    const float f = exp2f(s * c - top);
+    for (int e = 0; e < E; ++e) acc[e] += f * __uint_as_float((uint32_t)v[lane * E + e] << 16);
+  }
+}
+
 // One CTA a row and query head: over the parts of its prefix and its own tokens,
 // out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i, in a fixed order.  A thread a
 // part for the weights, then a warp a part for the values, four parts in flight.
-template <int DIM, int kJoinWarps>
+// CHUNK: more than one new token a sequence.
+template <int DIM, int kJoinWarps, bool CHUNK>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     join_kernel(const __grid_constant__ AttentionParams p) {
   constexpr int E = DIM / 32, kJoinThreads = kJoinWarps * 32;
@@ -1328,7 +1359,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   wait_prerequisites();
   Side far, own;
   far.n = own.n = 0;
+  int group = -1;
   const int fresh = fresh_of(b, seq);
+  uint16_t q[E] = {};   // read before any warp writes: out may be q itself
+  if (CHUNK) {
+    const uint16_t* src = static_cast<const uint16_t*>(p.q.data) +
+                          (int64_t)token * p.q.token_stride + (int64_t)head * p.q.head_stride;
+    if (E == 4) {
+      const uint2 v = reinterpret_cast<const uint2*>(src)[lane];
+      q[0] = (uint16_t)v.x, q[1] = (uint16_t)(v.x >> 16);
+      q[2 % E] = (uint16_t)v.y, q[3 % E] = (uint16_t)(v.y >> 16);
+    } else {
+      const uint32_t v = reinterpret_cast<const uint32_t*>(src)[lane];
+      q[0] = (uint16_t)v, q[1] = (uint16_t)(v >> 16);
+    }
+  }
   if (i < fresh) {
     // (Tokens that no table holds have no parts: what the workspace says is then old.)
     if (b.lens[seq] > 0 && b.table_width > 0)
@@ -1351,6 +1396,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         if (__shfl_sync(kAll, len, from) > 0 && b.prefix_width > 0)
           far = side_of(p, true, (end - first) * p.seq_rows, (seq - first) * p.seq_rows + in_seq,
                         kvh, item);
+        group = g0 + from;
         break;
       }
     }
@@ -1437,6 +1483,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) lo += values[w][e], hi += values[w][e + 1];
     *reinterpret_cast<uint32_t*>(out + e) = pack_bf16(lo * inv, hi * inv);
+    // NaN with a sum that is none, and tokens of this call behind the row's own: their
+    // V may be what is not finite.  The warp works its 64 elements out again.
+    if (CHUNK && i + 1 < fresh && sum == sum && __any_sync(kAll, lo != lo || hi != hi)) {
+      float again[E];
+      for (int j = 0; j < E; ++j) again[j] = 0.f;
+      if (group >= 0)
+        add_seen<DIM>(p, b.prefix_table + (int64_t)group * b.prefix_stride,
+                      capped(p, b.prefix_lens[group], b.prefix_width), kvh, q, top, again);
+      add_seen<DIM>(p, b.table + (int64_t)seq * b.table_stride,
+                    capped(p, max(b.lens[seq], 0) - fresh + i + 1, b.table_width), kvh, q, top,
+                    again);
+      if (lane * E / 64 == warp)
+        for (int j = 0; j < E; j += 2)
+          *reinterpret_cast<uint32_t*>(out + lane * E + j) =
+              pack_bf16(again[j] * inv, again[j + 1] * inv);
+    }
   }
   if (p.lse && threadIdx.x == 0)
     p.lse[(int64_t)token * p.heads + head] = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
@@ -1476,8 +1538,11 @@ cudaError_t launch_dim(const AttentionParams& p, const PageMaps& maps, cudaStrea
       dim3((unsigned)(p.batch.sequences * p.batch.chunk), (unsigned)p.heads);  // <= 2^24, 2^12
   cfg.blockDim = dim3((unsigned)(32 * warps));
   cfg.dynamicSmemBytes = 0;
-  return warps == 8 ? cudaLaunchKernelEx(&cfg, join_kernel<DIM, 8>, p)
-                    : cudaLaunchKernelEx(&cfg, join_kernel<DIM, 2>, p);
+  if (p.batch.chunk == 1)
+    return warps == 8 ? cudaLaunchKernelEx(&cfg, join_kernel<DIM, 8, false>, p)
+                      : cudaLaunchKernelEx(&cfg, join_kernel<DIM, 2, false>, p);
+  return warps == 8 ? cudaLaunchKernelEx(&cfg, join_kernel<DIM, 8, true>, p)
+                    : cudaLaunchKernelEx(&cfg, join_kernel<DIM, 2, true>, p);
 }
 
 uint64_t up256(uint64_t x) { return (x + 255) & ~255ull; }

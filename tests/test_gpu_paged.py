@@ -458,6 +458,37 @@ def test_attend_infinite_keys(paged):
     assert not got[1].any() and lse[1, 0] == -math.inf
 
 
+@pytest.mark.parametrize("lens,chunk,q_lens,heads,kw", [
+    ([40, 9, 7], 3, [3, 2, 3], 4, {}),
+    ([150, 33], 8, None, 8, dict(kv_heads=8, dim=128, prefix=[70], starts=[0, 1])),
+    ([300, 20], 20, [20, 12], 8, dict(prefix=[129], starts=[0, 2], page=32, dim=128)),
+    ([400], 200, None, 2, dict(kv_heads=1, page=8))])
+@pytest.mark.parametrize("scale", [0.125, -0.2])
+def test_attend_values_that_are_not_finite(paged, lens, chunk, q_lens, heads, kw, scale):
+    """An infinite or NaN V reaches the rows that see its token, and no other."""
+    c = Case(paged, 21, lens, q_lens=q_lens, **kw)
+    dim = c.k.shape[3]
+    for b, n in enumerate(lens):
+        fresh = chunk if q_lens is None else q_lens[b]
+        for back, d, x in ((1, 0, math.inf), (2, 5, math.nan), (fresh // 2 + 1, 9, -math.inf),
+                           (fresh // 2 + 1, dim - 1, math.inf)):
+            if back <= fresh:
+                page = c.k.shape[1]
+                c.v[c.table[b, (n - back) // page].long(), (n - back) % page, b % c.k.shape[2], d] = x
+    q = randn(c.g, len(lens) * chunk, heads, dim).bfloat16()
+    got, lse = c.kv.attend(c.batch, q, scale=scale, return_lse=True)
+    want, bound, want_lse, lse_bound = c.want(q, scale)
+    fine = torch.isfinite(want)
+    assert not fine.all()
+    assert ref.close(got[fine], want[fine], bound[fine], torch.bfloat16)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[torch.isinf(want)].double(), want[torch.isinf(want)])
+    seen = torch.isfinite(want_lse)
+    assert bool(((lse.double() - want_lse).abs()[seen] <= lse_bound[seen]).all())
+    assert c.kv.attend(c.batch, q, out=q, scale=scale) is q     # in place, to the bit
+    assert torch.equal(bits(q), bits(got)) and c.kv.device_error() == (0, 0)
+
+
 def test_attend_missing_pages(paged):
     """A page outside the pool counts as zeros and is reported, tokens past the
     table are not seen."""
