@@ -11,14 +11,15 @@
 // elements that rotate into each other, so that the rotation needs no exchange and
 // the norm one butterfly.  A block takes a few tokens: it works out their places and
 // each angle once, into shared memory, then its warps run over the tokens' heads,
-// loading the next while they turn the last.  A prompt is bound by issue slots (66 %
-// busy at 0.6 of a copy's rate), a few tokens by the chain of loads, so those get a
-// block for every four warps' heads.
+// loading the next while they turn the last.  A prompt is bound by its 18 warps an SM
+// (what registers leave) at 2.6 instructions a cycle, 0.6 of a copy's rate; a few tokens
+// by the chain of loads, so those get a block for every four warps' heads.
 //
 // B200, 32 + 8 heads of 128: q and k of 8192 tokens from BF16 42 us (168 MB, 4.0 TB/s);
 // appending 4 x 1024 rows of which 2519 are real 21 us; 64 tokens 3.8 us, one 3.2 us.
-// Five blocks an SM measured best (four 46 us, six 46), as did four tokens a block
-// (eight 52 us).
+// Five blocks an SM measured best (four 46 us, six 46), as did four tokens a block (eight
+// 52 us; twelve 41, but 40 for the ragged append), and eight elements a lane (sixteen,
+// with fewer instructions and fewer warps: 43).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
