@@ -17,8 +17,8 @@
 //
 // B200, 32 + 8 heads of 128: q and k of 8192 tokens from BF16 42 us (168 MB, 4.0 TB/s);
 // appending 4 x 1024 rows of which 2519 are real 21 us; 64 tokens 3.8 us, one 3.2 us.
-// Five blocks an SM measured best (four 46 us, six 46), as did four tokens a block (eight
-// 52 us; twelve 41, but 40 for the ragged append), and eight elements a lane (sixteen,
+// Five blocks an SM measured best (four 45 us, six 46), as did four tokens a block (eight
+// 48 us; twelve 41, but 40 for the ragged append), and eight elements a lane (sixteen,
 // with fewer instructions and fewer warps: 43).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
