@@ -33,6 +33,8 @@ _RAW.nwc_qk_norm_rope.argtypes = [_P] * 4 + [_I] * 4 + [_P, _I, _P, _P]
 _RAW.nwc_kv_append.argtypes = [_P] * 4 + [_I] + [_P] * 4
 _RAW.nwc_kv_attention.argtypes = [_P, _P, _P, _I, ctypes.c_float, _P, _P, _P, ctypes.c_uint64, _P]
 _check = _lib._check
+_Tensor, _grad_enabled, _empty = torch.Tensor, torch.is_grad_enabled, torch.empty_strided
+_bfloat16 = torch.bfloat16
 _TYPES = {torch.bfloat16: _lib.NWC_TYPE_BF16, torch.float32: _lib.NWC_TYPE_F32}
 _HEADS = ctypes.sizeof(_lib.nwc_heads)
 _ROPE = ctypes.sizeof(_lib.nwc_rope)
@@ -63,7 +65,7 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, device="cuda",
 
 
 def _no_grad(*tensors) -> None:
-    if torch.is_grad_enabled():
+    if _grad_enabled():
         for t in tensors:
             if isinstance(t, torch.Tensor) and t.requires_grad:
                 raise ValueError("a tensor requires a gradient, which these kernels do not "
@@ -75,7 +77,7 @@ def _heads(t, what: str, shape, device, dtypes=_TYPES, wide: bool = False,
     """The C view of a tensor [tokens, heads, dim] with any strides but a
     contiguous last dimension; wide: moved 16 bytes at a time; output: no two
     elements at one place."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
     dtype = t.dtype
     if dtype not in dtypes:
@@ -102,16 +104,17 @@ def _heads(t, what: str, shape, device, dtypes=_TYPES, wide: bool = False,
     return _pack_heads(_HEADS, _TYPES[dtype], at, ts, hs)
 
 
-def _new(like, shape):
-    """A new BF16 tensor of the shape of `like`, [tokens, heads, dim], and its C view."""
-    t = torch.empty_like(like, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
-    dim = shape[2]
-    return t, _pack_heads(_HEADS, 0, t.data_ptr(), shape[1] * dim, dim)
+def _new(device, shape):
+    """A new BF16 tensor of a shape [tokens, heads, dim], and its C view."""
+    _, heads, dim = shape
+    row = heads * dim
+    t = _empty(shape, (row, dim, 1), dtype=_bfloat16, device=device)
+    return t, _pack_heads(_HEADS, 0, t.data_ptr(), row, dim)
 
 
 def _vector(t, what: str, device, n: int, dtypes) -> int:
     """The address of a contiguous vector of n elements."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
@@ -171,13 +174,15 @@ def _raw_stream(index: int) -> int:
     return torch.cuda.current_stream(index).cuda_stream
 
 
-# The same handle without building a torch.cuda.Stream (3 us less a call).
+# The same without building a torch.cuda.Stream (3 us less a call), and the current
+# device without asking whether CUDA has been initialised.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(device, stream, call):
     """call(raw stream) where it should run."""
-    if stream is None and torch.cuda.current_device() == device.index:
+    if stream is None and _current_device() == device.index:
         return call(_raw_stream(device.index))
     with _On(device, stream) as raw:
         return call(raw)
@@ -186,7 +191,7 @@ def _on(device, stream, call):
 def _cuda(t, what: str):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what}: on {t.device}, expected a CUDA device")
     return t.device
 
@@ -223,9 +228,9 @@ def qk_norm_rope(q, k, positions, freq=None, q_weight=None, k_weight=None, eps: 
         qo = ko = qoh = koh = None
         if out is None:
             if q is not None:
-                qo, qoh = _new(q, (tokens, heads, dim))
+                qo, qoh = _new(device, (tokens, heads, dim))
             if k is not None:
-                ko, koh = _new(k, (tokens, kv_heads, dim))
+                ko, koh = _new(device, (tokens, kv_heads, dim))
         else:
             qo, ko = out
             if (qo is None) != (q is None) or (ko is None) != (k is None):
@@ -403,7 +408,7 @@ class PagedKV:
             if q_out is not None:
                 qoh = _heads(q_out, "q_out", shape, device, _BF16, output=True)
             elif q is not None:
-                q_out, qoh = _new(q, shape)
+                q_out, qoh = _new(device, shape)
             if rows:
                 _check(_RAW.nwc_kv_append(self._at, view, qh, qoh, heads, kh, vh, rope, raw),
                        "nwc_kv_append")
@@ -432,7 +437,7 @@ class PagedKV:
 
         def call(raw, out=out):
             if out is None:
-                out, oh = _new(q, shape)
+                out, oh = _new(self.device, shape)
             else:
                 oh = _heads(out, "out", shape, self.device, _BF16, wide=True, output=True)
             lse = torch.empty((rows, heads), dtype=torch.float32,
