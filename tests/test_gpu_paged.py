@@ -489,6 +489,28 @@ def test_attend_values_that_are_not_finite(paged, lens, chunk, q_lens, heads, kw
     assert torch.equal(bits(q), bits(got)) and c.kv.device_error() == (0, 0)
 
 
+@pytest.mark.parametrize("lens,chunk,heads,kw", [
+    ([40, 9], 3, 4, {}), ([300, 20], 20, 8, dict(prefix=[129], starts=[0, 2], dim=128)),
+    ([400], 200, 2, dict(kv_heads=1, page=8))])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attend_keys_that_are_not_finite(paged, lens, chunk, heads, kw, bad):
+    """So does such a K: the rows before its token are right."""
+    c = Case(paged, 22, lens, **kw)
+    page, back = c.k.shape[1], chunk // 2
+    for b, n in enumerate(lens):
+        c.k[c.table[b, (n - back) // page].long(), (n - back) % page, :, 3] = bad
+    q = randn(c.g, len(lens) * chunk, heads, c.k.shape[3]).bfloat16()
+    got, lse = c.kv.attend(c.batch, q, return_lse=True)
+    want, bound, want_lse, lse_bound = c.want(q, c.k.shape[3] ** -0.5)
+    before = (torch.arange(chunk, device="cuda") < chunk - back).repeat(len(lens))
+    assert torch.isfinite(want[before]).all()
+    assert ref.close(got[before], want[before], bound[before], torch.bfloat16)
+    assert bool(((lse.double() - want_lse).abs()[before] <= lse_bound[before]).all())
+    if math.isnan(bad):
+        assert torch.isnan(got[~before]).all()
+    assert c.kv.device_error() == (0, 0)
+
+
 def test_attend_missing_pages(paged):
     """A page outside the pool counts as zeros and is reported, tokens past the
     table are not seen."""
