@@ -548,6 +548,29 @@ def test_attend_bounded_waits(paged):
     c.check(q, got, lse)
 
 
+@pytest.mark.parametrize("limit", [1, 30, 300])
+@pytest.mark.parametrize("lens,chunk,heads,kw", [
+    ([400] * 3, 150, 8, dict(kv_heads=4, dim=128, prefix=[900], starts=[0, 3])),   # both teams
+    ([700] * 12, 1, 32, dict(kv_heads=2, prefix=[1500, 300], starts=[0, 9, 11])),  # every kind
+    ([2000], 64, 8, dict(kv_heads=4, page=64))])                                   # one team
+def test_attend_bounded_waits_of_every_kind(paged, limit, lens, chunk, heads, kw):
+    """Waits that give up at the first poll or further on, in parts of every kind of
+    rows: the kernel returns, and the next call is right."""
+    from lossless_bf16_weight_nwc_b200 import _lib
+    c = Case(paged, 23, lens, **kw)
+    q = randn(c.g, len(lens) * chunk, heads, c.kv.dim).bfloat16()
+    _lib.nwc_test_set_wait_limit(limit)
+    try:
+        for _ in range(3):
+            c.kv.attend(c.batch, q)
+        status, word = c.kv.device_error()
+    finally:
+        _lib.nwc_test_set_wait_limit(0)
+    assert (status, word) in ((6, 1), (0, 0)) and (word or limit > 1)
+    got, lse = c.kv.attend(c.batch, q, return_lse=True)
+    c.check(q, got, lse)
+
+
 def test_attend_tables_without_columns_after_others(paged):
     """Lengths that no table holds leave nothing to see, whatever an earlier call of
     the same shape left in the workspace."""
