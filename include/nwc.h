@@ -414,7 +414,10 @@ typedef struct {
  *     d_prefix_lens[g] tokens in pages d_prefix_table[g prefix_stride + n],
  *     n < prefix_width, which comes before their own tokens.  Sequences in no
  *     group have no prefix.  groups = 0: none has.
- * Lengths below zero count as zero.  A token beyond its table (or the 2^30th), or
+ * Lengths below zero count as zero.  A real row whose index is then negative (more
+ * new tokens than the sequence has) has no place: it is not appended, its q is normed
+ * and rotated at its position, and in attention it sees its prefix and no own token.
+ * A token beyond its table (or the 2^30th), or
  * on a page outside [0, pages), sets error bit 4: it is not appended, and
  * attention sees no token past the table and zeros for the page.
  * sequences x new_tokens <= 2^24; groups <= sequences.  A table of width 0 holds no

@@ -112,7 +112,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, bool vec, const float (
 struct Place {
   bool real;         // a new token (not padding)
   int64_t position;  // in the whole text: prefix + own index
-  int64_t slot_page; // its page, or -1 when the tables do not hold it
+  int64_t slot_page; // its page, or -1 when it has none or the tables do not hold it
   int32_t slot;      // its place in the page
 };
 __device__ __forceinline__ Place place_of(const CacheView& c, const BatchView& b, int row,
@@ -122,7 +122,7 @@ __device__ __forceinline__ Place place_of(const CacheView& c, const BatchView& b
   const int len = max(b.lens[seq], 0);
   const int fresh = b.q_lens ? min(max(b.q_lens[seq], 0), b.chunk) : b.chunk;
   const int j = len - fresh + i;
-  at.real = i < fresh && j >= 0;
+  at.real = i < fresh;
   int64_t base = 0;
   for (int g0 = 0; g0 < b.groups; g0 += 32) {  // the group that holds the sequence
     const int g = g0 + lane;
@@ -136,7 +136,7 @@ __device__ __forceinline__ Place place_of(const CacheView& c, const BatchView& b
   at.position = base + j;
   at.slot = j & ((1 << c.page_shift) - 1);
   at.slot_page = -1;
-  if (at.real) {
+  if (at.real && j >= 0) {   // before the sequence's start there is no place
     const int n = j >> c.page_shift;
     if (n < b.table_width && j < (1 << 30)) at.slot_page = b.table[(int64_t)seq * b.table_stride + n];
     if (at.slot_page < 0 || at.slot_page >= c.pages) {

@@ -256,7 +256,11 @@ class PagedBatch:
     block_table  int32 [sequences, width]: sequence b's own pages, in order.
     seq_lens     int32 [sequences]: own tokens, a call's new ones among them.
     q_lens       int32 [sequences] or None: how many of a sequence's rows are
-                 new tokens, from its first row; the others are padding.
+                 new tokens, from its first row; the others are padding.  New
+                 tokens that seq_lens does not count (the first, where it counts
+                 fewer) have no place: they are not appended, their q still turns
+                 at its position (the prefix's length plus an index below zero)
+                 and sees the prefix alone.
     prefix_table int32 [groups, width], prefix_lens int32 [groups], group_start
                  int32 [groups + 1]: sequences group_start[g] up to
                  group_start[g + 1] share prefix g, which comes before their own

@@ -341,6 +341,37 @@ def test_append_without_q_or_rotation(paged):
     assert torch.equal(c.k[p, s], k.bfloat16()) and torch.equal(c.v[p, s], v.bfloat16())
 
 
+@pytest.mark.parametrize("lens,chunk,q_lens", [
+    ([0, 2, 1, 0, 5], 1, None), ([0, 2, 1, -4, 5], 3, None), ([0, 2, 1, 3, 5], 3, [0, 3, 2, 3, 1]),
+    ([3] * 500, 4, None)])
+def test_rows_before_a_sequences_start(paged, lens, chunk, q_lens):
+    """More new tokens than a sequence has: those before its start are not appended;
+    their q is that of their position, and they see the prefix, where there is one."""
+    n = len(lens)
+    c = Case(paged, 24, lens, q_lens=q_lens, prefix=[20, 40], starts=[0, 2, n - 1])
+    q, k, v = (randn(c.g, n * chunk, h, 64) for h in (4, 2, 2))
+    freq, w = paged.rope_frequencies(64, 1e4), weights(c.g, "bf16", 64)
+    k0, v0 = c.k.clone(), c.v.clone()
+    got = c.kv.append(c.batch, k, v, q=q, freq=freq, q_weight=w, k_weight=w)
+    fresh = torch.tensor(q_lens or [chunk] * n, device="cuda")[:, None]
+    i = torch.arange(chunk, device="cuda")
+    j = torch.tensor(lens, device="cuda").clamp(min=0)[:, None] - fresh + i
+    base = torch.tensor([20] * 2 + [40] * (n - 3) + [0], device="cuda")[:, None]
+    pos, real = (base + j).flatten(), (i < fresh).flatten()
+    want, bound = ref.norm_rotate(q, w, pos, freq, False, 1e-6)
+    assert ref.close(got[real], want[real], bound[real], torch.bfloat16) and not got[~real].any()
+    on = real & (j >= 0).flatten()
+    rows, at = torch.arange(n, device="cuda").repeat_interleave(chunk)[on], j.flatten()[on]
+    place = (c.table[rows, at // 16].long(), at % 16)
+    want, bound = ref.norm_rotate(k, w, pos, freq, False, 1e-6)
+    assert ref.close(c.k[place], want[on], bound[on], torch.bfloat16)
+    assert torch.equal(c.v[place], v[on].bfloat16())
+    o, lse = c.kv.attend(c.batch, got, return_lse=True)
+    c.check(got, o, lse)
+    c.k[place], c.v[place] = k0[place], v0[place]
+    assert torch.equal(bits(c.k), bits(k0)) and torch.equal(bits(c.v), bits(v0))
+
+
 def test_append_outside_the_tables(paged):
     """Pages that are not there and lengths past the table: nothing is written."""
     c = Case(paged, 5, [20, 20, 20, 20], poison=False, width=2)
