@@ -1317,6 +1317,23 @@ __device__ __forceinline__ Side side_of(const AttentionParams& p, bool far, int 
   return d;
 }
 
+// Whether V of a token in [from, to) of a sequence holds what is not finite in this head
+// (a warp; pages that are not there count as zeros).
+template <int DIM>
+__device__ __noinline__ bool any_not_finite(const AttentionParams& p, const int32_t* table,
+                                            int from, int to, int kvh) {
+  const CacheView& cv = p.cache;
+  const int lane = threadIdx.x & 31, mask = (1 << cv.page_shift) - 1;
+  for (int j = from; j < to; ++j) {
+    const int64_t page = table[j >> cv.page_shift];
+    if (page < 0 || page >= cv.pages) continue;
+    const uint16_t* v = cv.v + page * cv.v_page + (j & mask) * cv.v_token + kvh * cv.v_head;
+    bool bad = false;
+    for (int e = lane; e < DIM; e += 32) bad |= (v[e] & 0x7F80) == 0x7F80;
+    if (__any_sync(kAll, bad)) return true;
+  }
+  return false;
+}
 // Weighted values of a segment's first `limit` tokens for one row, by a warp token by
 // token, E elements a lane, with the row's maximum known: for rows where a V that they do
 // not see spoilt the products (zero times infinity is not zero).
@@ -1488,17 +1505,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) lo += values[w][e], hi += values[w][e + 1];
     *reinterpret_cast<uint32_t*>(out + e) = pack_bf16(lo * inv, hi * inv);
-    // NaN with a sum that is none, and tokens of this call behind the row's own: their
-    // V may be what is not finite.  The warp works its 64 elements out again.
+    // NaN with a sum that is none, and tokens of this call behind the row's own: where
+    // their V is what is not finite, the warp works its 64 elements out again.  (A V that
+    // the row sees needs no such pass, which takes milliseconds over 32768 tokens.)
     if (CHUNK && i + 1 < fresh && sum == sum && __any_sync(kAll, lo != lo || hi != hi)) {
+      const int32_t* table = b.table + (int64_t)seq * b.table_stride;
+      const int len = max(b.lens[seq], 0);
+      const int seen = capped(p, len - fresh + i + 1, b.table_width);
+      if (!any_not_finite<DIM>(p, table, seen, capped(p, len, b.table_width), kvh)) continue;
       float again[E];
       for (int j = 0; j < E; ++j) again[j] = 0.f;
       if (group >= 0)
         add_seen<DIM>(p, b.prefix_table + (int64_t)group * b.prefix_stride,
                       capped(p, b.prefix_lens[group], b.prefix_width), kvh, q, top, again);
-      add_seen<DIM>(p, b.table + (int64_t)seq * b.table_stride,
-                    capped(p, max(b.lens[seq], 0) - fresh + i + 1, b.table_width), kvh, q, top,
-                    again);
+      add_seen<DIM>(p, table, seen, kvh, q, top, again);
       if (lane * E / 64 == warp)
         for (int j = 0; j < E; j += 2)
           *reinterpret_cast<uint32_t*>(out + lane * E + j) =
