@@ -984,10 +984,11 @@ __device__ bool few_part(const AttentionParams& p, const Part& part, uint8_t* sm
   return __all_sync(kAll, wait(&bars->team[w], (*meets)++ & 1u, ctl));
 }
 
-// Scores are in units of log2; a scale of zero is replaced by one that leaves every
-// finite score at zero (so that masked scores of -inf stay what they are).
+// Scores are in units of log2; a scale of zero is replaced by the least FP32 number,
+// which leaves every finite score below 2^-20 (so that masked scores of -inf stay what
+// they are).
 __device__ __forceinline__ float score_unit(float scale) {
-  return fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-38f);
+  return fmaxf(fabsf(scale) * 1.4426950408889634f, 0x1p-149f);
 }
 
 // A softmax team: thread r has row r of the team's rows.

@@ -459,6 +459,28 @@ def test_attend_scales(paged, scale):
     c.check(q, got, lse, scale)
 
 
+@pytest.mark.parametrize("chunk,heads", [(1, 1), (3, 8), (40, 4)])
+@pytest.mark.parametrize("scale", [0.0, 1e-45, -1e-40, 2.0 ** -120])
+def test_attend_tiny_scales(paged, chunk, heads, scale):
+    """Scales near and at zero with products near FP32's largest: a scale of zero weighs
+    every token alike, whatever its product."""
+    c = Case(paged, 26, [60, 300], kv_heads=1, dim=64, prefix=[200], starts=[0, 1])
+    q = torch.zeros((2 * chunk, heads, 64), device="cuda").bfloat16()
+    c.k[torch.isfinite(c.k)] *= 2.0 ** -20
+    q[..., 0] = 2.0 ** 62
+    for row, n in ((c.table[0], 60), (c.table[1], 300), (c.far[0], 200)):
+        at = torch.arange(0, n, 3, device="cuda")
+        c.k[row[at // 16].long(), at % 16, :, 0] = 2.0 ** 64      # products of 2^126
+    got, lse = c.kv.attend(c.batch, q, scale=scale, return_lse=True)
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    want, bound, want_lse, lse_bound = c.want(q, scale)
+    # The least FP32 number as scale moves a weight by less than 2^-20 of itself.
+    size = torch.nan_to_num(c.v.float(), 0, 0, 0).abs().max()
+    assert ref.close(got, want, bound + 2.0 ** -19 * size, torch.bfloat16)
+    assert bool(((lse.double() - want_lse).abs() <= lse_bound + 2.0 ** -19).all())
+    assert c.kv.device_error() == (0, 0)
+
+
 def test_attend_rising_scores(paged):
     """A running maximum that grows by more than any fixed step tile after tile."""
     c = Case(paged, 7, [1500], kv_heads=1, dim=64, prefix=[1024], starts=[0, 1])
