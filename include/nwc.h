@@ -464,6 +464,7 @@ nwc_status nwc_kv_attention_workspace(const nwc_kv_cache* cache, const nwc_kv_ba
  *   q, out: [rows][heads][dim], BF16, 16-byte aligned with strides of 8
  *     elements; out may be q.  heads: a multiple of kv_heads; rows x heads / kv_heads <= 2^30.
  *     dim: 64 or 128 (others: UNSUPPORTED).
+ *   scale: of any sign; scale / ln 2 must be finite in FP32.
  *   d_lse (or NULL): FP32 [rows][heads], the natural logarithm of the sum of
  *     exp(scale q . K) over the row's tokens.
  *   d_workspace: at least nwc_kv_attention_workspace bytes, 256-byte aligned;

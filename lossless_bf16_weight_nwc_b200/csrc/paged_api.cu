@@ -221,8 +221,8 @@ nwc_status nwc_kv_attention(const nwc_kv_cache* cache, const nwc_kv_batch* batch
                             const nwc_heads* out, float* d_lse, void* d_workspace,
                             uint64_t workspace_bytes, nwc_stream_t stream) {
   if (!attention_shape(cache, batch, heads) || !wide_heads(q) || !wide_heads(out) ||
-      !std::isfinite(scale) || !aligned_to(d_lse, 4))
-    return NWC_ERR_INVALID_ARG;
+      !std::isfinite(scale * 1.4426950408889634f) || !aligned_to(d_lse, 4))
+    return NWC_ERR_INVALID_ARG;   // (the kernels' scores are in units of log2)
   if (cache->dim != 64 && cache->dim != 128) return NWC_ERR_UNSUPPORTED;
   if (batch->sequences == 0) return NWC_OK;
   int dev, sms;

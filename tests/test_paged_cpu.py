@@ -140,6 +140,15 @@ def test_attention_arguments(lib):
     assert lib.LIB.nwc_kv_get_error(None, None, None) == INVALID
 
 
+def test_attention_scales(lib):
+    """Refused where the kernel's own unit, scale / ln 2, would be infinite."""
+    q, out = heads(lib, 0), heads(lib, 0)
+    for scale, want in ((2e38, OK), (-2e38, OK), (0.0, OK), (2.4e38, INVALID), (-3e38, INVALID)):
+        got = lib.LIB.nwc_kv_attention(cache(lib), batch(lib), q, 16, scale, out, None, 0x10000,
+                                       1 << 40, None)
+        assert got == want, scale
+
+
 def test_python_calls_refuse_host_tensors_and_gradients(lib):
     from lossless_bf16_weight_nwc_b200 import paged
     q = torch.zeros(2, 4, 64)
