@@ -99,7 +99,8 @@ def _heads(t, what: str, shape, device, dtypes=_TYPES, wide: bool = False,
         raise ValueError(f"{what}: needs 16-byte alignment and strides of multiples of 8 elements")
     if output and tokens and not (
             (heads < 2 or hs >= dim) and (tokens < 2 or ts >= dim) and
-            (heads < 2 or tokens < 2 or ts >= heads * hs or hs >= tokens * ts)):
+            (heads < 2 or tokens < 2 or ts >= (heads - 1) * hs + dim or
+             hs >= (tokens - 1) * ts + dim)):
         raise ValueError(f"{what}: its elements overlap")
     return _pack_heads(_HEADS, _TYPES[dtype], at, ts, hs)
 

@@ -212,6 +212,22 @@ def test_tensor_checks(lib):
         paged._rope(64, cpu, f, None, None, -1.0, False)
 
 
+def test_outputs_with_gaps(lib):
+    """Every layout without two elements at one place is an output: the last head or
+    token need not bring its gap with it."""
+    from lossless_bf16_weight_nwc_b200 import paged
+    cpu = torch.device("cpu")
+    t = torch.zeros(3, 5, 64)
+    for out in (t[:, ::2], t[..., 8:], t.transpose(0, 1)[:, ::2], t[::2].transpose(0, 1),
+                torch.as_strided(t, (2, 2, 8), (24, 16, 1)),
+                torch.as_strided(t, (2, 2, 8), (16, 24, 1))):
+        paged._heads(out, "o", out.shape, cpu, output=True)
+    for strides in ((23, 16, 1), (16, 23, 1), (7, 24, 1), (24, 7, 1)):
+        bad = torch.as_strided(t, (2, 2, 8), strides)
+        with pytest.raises(ValueError, match="overlap"):
+            paged._heads(bad, "o", bad.shape, cpu, output=True)
+
+
 def test_rope_frequencies(lib):
     from lossless_bf16_weight_nwc_b200 import paged
     f = paged.rope_frequencies(128, 5e5, "cpu")
