@@ -373,7 +373,9 @@ typedef struct {
 /* q_out[t] = rotate(norm(q[t]), positions[t]) and k_out likewise, t < tokens.
  *   q, q_out: [tokens][heads][dim]; k, k_out: [tokens][kv_heads][dim].  q and k
  *     have one type, q_out and k_out one type.  q (with q_out) or k (with k_out)
- *     may be NULL.  In place (q_out = q with the same strides) is allowed.
+ *     may be NULL.  In place (q_out = q with the same type and strides, k_out = k
+ *     likewise) is allowed; an output that overlaps anything else of the call is not
+ *     (nor is it in the calls below).
  *   d_positions: int32 [tokens], or int64 when positions_64 is non-zero; any
  *     sign.
  *   dim: a multiple of 8 up to 256.  tokens in [0, 2^24]; 0 launches nothing.

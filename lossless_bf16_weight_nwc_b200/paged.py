@@ -105,6 +105,62 @@ def _heads(t, what: str, shape, device, dtypes=_TYPES, wide: bool = False,
     return _pack_heads(_HEADS, _TYPES[dtype], at, ts, hs)
 
 
+def _meet(a, b) -> bool:
+    """Whether two tensors [tokens, heads, dim] hold a byte in common; told apart where
+    their strides are the same (views of one tensor), else taken to be so."""
+    steps = []
+    for d in (0, 1):   # (step in bytes, the most that b is steps behind a, and before it)
+        n, m = a.shape[d], b.shape[d]
+        s, t = a.stride(d) * a.element_size(), b.stride(d) * b.element_size()
+        s, t = (t if n < 2 else s), (s if m < 2 else t)
+        if s != t:
+            return True
+        if s and (n > 1 or m > 1):
+            steps.append((s, n - 1, m - 1))
+    steps.sort(reverse=True)
+    wide, width = a.shape[2] * a.element_size(), b.shape[2] * b.element_size()
+
+    def any_at(apart, k):   # b's first byte lies `apart` behind a's
+        if k == len(steps):
+            return -width < apart < wide
+        # The steps k + 1, ... change `apart` by -down to up.
+        down = sum(s * n for s, n, _ in steps[k + 1:])
+        up = sum(s * m for s, _, m in steps[k + 1:])
+        s, n, m = steps[k]
+        first = max(-n, -((apart + up + width - 1) // s))
+        last = min(m, (down + wide - 1 - apart) // s)
+        return any(any_at(apart + i * s, k + 1) for i in range(first, last + 1))
+
+    return any_at(b.data_ptr() - a.data_ptr(), 0)
+
+
+def _bytes(t):
+    """A tensor's first byte and the one behind its last."""
+    at, last = t.data_ptr(), 0
+    for n, s in zip(t.shape, t.stride()):
+        if n == 0:
+            return at, at
+        last += (n - 1) * s
+    return at, at + (last + 1) * t.element_size()
+
+
+def _apart(out, what: str, source, *others) -> None:
+    """Refuses an output in memory of another tensor of its call, whose kernels read
+    while they write; `source` (an input of its shape) may be the output itself."""
+    at, end = _bytes(out)
+    for t in (source, *others):
+        if t is None:
+            continue
+        first, behind = _bytes(t)
+        if behind <= at or end <= first or first == behind or at == end:
+            continue
+        if (t is source and first == at and t.dtype == out.dtype and
+                all(n < 2 or s == o for n, s, o in zip(t.shape, t.stride(), out.stride()))):
+            continue
+        if t.dim() != 3 or _meet(out, t):
+            raise ValueError(f"{what}: overlaps another tensor of the call")
+
+
 def _new(device, shape):
     """A new BF16 tensor of a shape [tokens, heads, dim], and its C view."""
     _, heads, dim = shape
@@ -205,8 +261,8 @@ def qk_norm_rope(q, k, positions, freq=None, q_weight=None, k_weight=None, eps: 
     rope_frequencies; None: no rotation) in pairs (i, i + rotary / 2), or
     (2i, 2i + 1) when interleaved.  q and k are FP32 or BF16 with any strides but
     a contiguous last dimension (views of a GEMV's result); either may be None.
-    The results are BF16, or what `out` (a pair of tensors, also q and k
-    themselves) holds."""
+    The results are BF16, or what `out` (a pair of tensors) holds: q and k
+    themselves, or memory of no other tensor of the call."""
     first = q if q is not None else k
     device = _cuda(first, "q" if q is not None else "k")
     _no_grad(q, k, freq, q_weight, k_weight, *(out or ()))
@@ -242,6 +298,11 @@ def qk_norm_rope(q, k, positions, freq=None, q_weight=None, k_weight=None, eps: 
             if k is not None:
                 koh = _heads(ko, "out[1]", (tokens, kv_heads, dim), device,
                              _TYPES if q is None else (qo.dtype,), output=True)
+            read = (positions, freq, q_weight, k_weight)
+            if q is not None:
+                _apart(qo, "out[0]", q, k, ko, *read)
+            if k is not None:
+                _apart(ko, "out[1]", k, q, *read)
         if tokens:
             _check(_RAW.nwc_qk_norm_rope(qh, kh, qoh, koh, tokens, heads, kv_heads, dim, at,
                                          positions.dtype == torch.int64, rope, raw),
@@ -390,7 +451,8 @@ class PagedKV:
         heads, dim], normed and rotated likewise, as BF16 (None without q).  Inputs
         FP32 or BF16, one type, with any strides but a contiguous last dimension.
         seq_lens counts the new tokens already.  Padding rows are not appended,
-        their q is zero."""
+        their q is zero.  q_out: q itself, or memory of no other tensor of the call
+        or the cache."""
         rows, view = self._rows(batch, k, "k")
         _no_grad(q, k, v, freq, q_weight, k_weight, q_out)
         device = self.device
@@ -412,6 +474,8 @@ class PagedKV:
         def call(raw, q_out=q_out, qoh=None):
             if q_out is not None:
                 qoh = _heads(q_out, "q_out", shape, device, _BF16, output=True)
+                _apart(q_out, "q_out", q, k, v, freq, q_weight, k_weight, self.k_pages,
+                       self.v_pages, *batch._keep)
             elif q is not None:
                 q_out, qoh = _new(device, shape)
             if rows:
@@ -427,7 +491,8 @@ class PagedKV:
         kv_heads; dim 64 or 128; scale None: 1 / sqrt(dim)): each row sees its
         prefix and its sequence's own tokens up to itself.  BF16 of q's shape;
         with return_lse also FP32 [rows, heads], the logarithm of the sum of
-        exponentials.  A row that sees nothing, and a padding row, is zero (-inf)."""
+        exponentials.  A row that sees nothing, and a padding row, is zero (-inf).
+        out: q itself, or memory of no other tensor of the call or the cache."""
         rows, view = self._rows(batch, q, "q")
         _no_grad(q, out)
         if self.dim not in (64, 128):
@@ -445,6 +510,7 @@ class PagedKV:
                 out, oh = _new(self.device, shape)
             else:
                 oh = _heads(out, "out", shape, self.device, _BF16, wide=True, output=True)
+                _apart(out, "out", q, self.k_pages, self.v_pages, *batch._keep)
             lse = torch.empty((rows, heads), dtype=torch.float32,
                               device=self.device) if return_lse else None
             if rows:

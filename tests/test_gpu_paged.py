@@ -333,6 +333,32 @@ def test_refusals_on_the_device(paged):
     assert c.kv.device_error() == (0, 0)
 
 
+def test_outputs_in_other_tensors_memory_are_refused(paged):
+    """Results over an input at another place, over each other or over the cache."""
+    c = Case(paged, 27, [9, 30], poison=False)
+    y = randn(c.g, 3, 8, 64).bfloat16()
+    q, k, v = y[:2, :4], y[:2, 4:6], y[:2, 6:]
+    freq, at = paged.rope_frequencies(64), ints([1, 2])
+    pages = c.k.view(-1, 4, 64)[:2]
+    for bad in (lambda: paged.qk_norm_rope(q, k, at, freq, out=(y[1:, :4], k)),
+                lambda: paged.qk_norm_rope(k, v, at, freq, out=(v, k)),
+                lambda: paged.qk_norm_rope(k, v, at, freq, out=(q[:, :2], q[:, 1:3])),
+                lambda: paged.qk_norm_rope(q, k, at, freq, out=(y[:2, 2:6], y[:2, :2])),
+                lambda: paged.qk_norm_rope(q.float(), None, at, freq[:4].clone(), q[0, 0],
+                                           out=(q, None)),
+                lambda: c.kv.append(c.batch, k, v, q=q, q_out=y[:2, 2:6]),
+                lambda: c.kv.append(c.batch, k, v, q=q, q_out=pages),
+                lambda: c.kv.attend(c.batch, q, out=y[1:, :4]),
+                lambda: c.kv.attend(c.batch, q, out=pages)):
+        with pytest.raises(ValueError, match="overlaps"):
+            bad()
+    k0, v0, want = c.k.clone(), v.clone(), paged.qk_norm_rope(q, k, at, freq)
+    got = paged.qk_norm_rope(q, k, at, freq, out=(q, k))       # in place, beside each other
+    assert got[0] is q and torch.equal(bits(q), bits(want[0]))
+    assert torch.equal(bits(k), bits(want[1])) and torch.equal(bits(v), bits(v0))
+    assert torch.equal(bits(c.k), bits(k0)) and c.kv.device_error() == (0, 0)
+
+
 def test_append_without_q_or_rotation(paged):
     c = Case(paged, 4, [4, 9], poison=False)
     k, v = randn(c.g, 2, 2, 64), randn(c.g, 2, 2, 64)

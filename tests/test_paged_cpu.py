@@ -228,6 +228,47 @@ def test_outputs_with_gaps(lib):
             paged._heads(bad, "o", bad.shape, cpu, output=True)
 
 
+def _bytes_of(t):
+    """Every byte of a tensor, one by one."""
+    at = [t.data_ptr()]
+    for n, s in zip(t.shape, t.stride()):
+        at = [a + i * s * t.element_size() for a in at for i in range(n)]
+    return {a + b for a in at for b in range(t.element_size())}
+
+
+def test_outputs_apart(lib):
+    """Two views of one memory, told apart byte by byte; the output itself as source."""
+    import random
+    from lossless_bf16_weight_nwc_b200 import paged
+    rng = random.Random(3)
+    base = torch.zeros(400, dtype=torch.bfloat16)
+    apart = met = 0
+    for _ in range(3000):
+        strides = rng.choice([(24, 8), (8, 24), (40, 10), (16, 16), (30, 0), (7, 3), (0, 0)])
+        a, b = (torch.as_strided(base, (rng.randint(1, 4), rng.randint(1, 3), rng.randint(1, 9)),
+                                 (*strides, 1), rng.randint(0, 150)) for _ in range(2))
+        both = not _bytes_of(a).isdisjoint(_bytes_of(b))
+        assert paged._meet(a, b) == both and paged._meet(b, a) == both
+        met, apart = met + both, apart + (not both)
+    assert min(met, apart) > 500
+    y = torch.zeros(5, 6 * 8).bfloat16()
+    q, k = y[:, :32].unflatten(1, (4, 8)), y[:, 32:].unflatten(1, (2, 8))
+    paged._apart(q, "o", q, k, None, torch.zeros(3))
+    paged._apart(k, "o", q, torch.zeros(0))
+    paged._apart(q[:1], "o", q[:1], k)                     # strides of one token do not count
+    paged._apart(torch.zeros(0, 4, 8).bfloat16(), "o", q)
+    paged._apart(torch.zeros(5, 4, 8), "o", q)
+    full = torch.zeros(10, 4, 8)
+    for out, source, others in (
+            (k, k, (q, y)), (q[1:], q[:-1], ()), (full[:5].bfloat16(), None, ()),
+            (torch.as_strided(full.view(torch.bfloat16), (5, 4, 8), (64, 16, 1)), full[:5], ()),
+            (torch.as_strided(full, (5, 4, 8), (32, 8, 1)), full[:5].transpose(0, 1), ()),
+            (full[:5], None, (full[4, 3],)), (q, q, (y[:, 31:40],))):
+        if others or source is not None:
+            with pytest.raises(ValueError, match="overlaps"):
+                paged._apart(out, "o", source, *others)
+
+
 def test_rope_frequencies(lib):
     from lossless_bf16_weight_nwc_b200 import paged
     f = paged.rope_frequencies(128, 5e5, "cpu")
