@@ -548,6 +548,18 @@ class AttentionBlock:
                              f"{cache.dim}")
         if wo.cols != b[1]:
             raise ValueError(f"wo: {wo.cols} columns, expected {b[1]}")
+        # What attend would refuse is refused here: a step would have appended by then.
+        heads = b[1] // cache.dim
+        if heads < 1 or heads % cache.kv_heads:
+            raise ValueError(f"wqkv: {heads} query heads, expected a multiple of {cache.kv_heads}")
+        if cache.dim not in (64, 128):
+            raise ValueError(f"dim {cache.dim}: attention takes heads of 64 or 128")
+        if scale is not None and not abs(scale) * 1.4426950408889634 < 2.0 ** 128:
+            raise ValueError("scale: a finite number, also divided by ln 2 in FP32")
+        for m, what in ((wqkv, "wqkv"), (wo, "wo")):
+            if m.image.device != cache.device:
+                raise ValueError(f"{what}: on {m.image.device}, expected {cache.device}")
+        _rope(cache.dim, cache.device, freq, q_weight, k_weight, eps, interleaved)
         self.wqkv, self.wo, self.cache, self.freq = wqkv, wo, cache, freq
         self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
         self.interleaved, self.scale = interleaved, scale

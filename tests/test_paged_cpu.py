@@ -228,6 +228,31 @@ def test_outputs_with_gaps(lib):
             paged._heads(bad, "o", bad.shape, cpu, output=True)
 
 
+def test_attention_block_arguments(lib):
+    """What a step would find out after it has appended is refused when the block is made."""
+    from types import SimpleNamespace as Fake
+    from lossless_bf16_weight_nwc_b200 import paged
+    cpu = torch.device("cpu")
+
+    def block(heads=8, kv_heads=2, dim=64, cols=None, wqkv_on=cpu, wo_on=cpu, splits=None, **kw):
+        b = splits or [0, heads * dim, (heads + kv_heads) * dim, (heads + 2 * kv_heads) * dim]
+        return paged.AttentionBlock(
+            Fake(row_splits=b, image=Fake(device=wqkv_on)),
+            Fake(cols=heads * dim if cols is None else cols, image=Fake(device=wo_on)),
+            Fake(kv_heads=kv_heads, dim=dim, device=cpu),
+            kw.pop("freq", torch.ones(dim // 2, dtype=torch.float64)), **kw)
+
+    block(), block(dim=128, scale=-1.0), block(kv_heads=1, heads=3, q_weight=torch.ones(64))
+    other = torch.device("cuda:0")
+    for bad in (dict(heads=7), dict(heads=0), dict(dim=32), dict(dim=80), dict(cols=64),
+                dict(scale=math.inf), dict(scale=math.nan), dict(scale=3e38), dict(eps=-1.0),
+                dict(wqkv_on=other), dict(wo_on=other), dict(splits=[0, 512]),
+                dict(freq=torch.ones(30, dtype=torch.float64)), dict(q_weight=torch.ones(32)),
+                dict(k_weight=torch.ones(64, device="meta"))):
+        with pytest.raises(ValueError):
+            block(**bad)
+
+
 def _bytes_of(t):
     """Every byte of a tensor, one by one."""
     at = [t.data_ptr()]
