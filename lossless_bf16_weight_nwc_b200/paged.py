@@ -13,7 +13,8 @@ A layer's step with a fused q/k/v matrix (`CompressedMatrix.compress_fused`):
 `AttentionBlock` holds those pieces for one layer.  All of it runs in libnwc's
 kernels; lengths and tables stay on the device, so a step can be captured into a
 CUDA graph and replayed as they change.  Nothing here has a gradient: inputs
-that require one are refused while gradients are recorded.
+that require one are refused while gradients are recorded, as are those with a
+forward-mode tangent.
 """
 from __future__ import annotations
 
@@ -22,6 +23,7 @@ import math
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 
@@ -70,6 +72,12 @@ def _no_grad(*tensors) -> None:
             if isinstance(t, torch.Tensor) and t.requires_grad:
                 raise ValueError("a tensor requires a gradient, which these kernels do not "
                                  "give; call under torch.no_grad()")
+    # (The level saves asking every tensor where no dual level is open.)
+    if getattr(forward_ad, "_current_level", 0) >= 0:
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("a tensor has a tangent, a forward-mode gradient that these "
+                                 "kernels do not carry on; unpack it first")
 
 
 def _heads(t, what: str, shape, device, dtypes=_TYPES, wide: bool = False,

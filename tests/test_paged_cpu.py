@@ -228,6 +228,21 @@ def test_outputs_with_gaps(lib):
             paged._heads(bad, "o", bad.shape, cpu, output=True)
 
 
+def test_tangents_are_refused(lib):
+    """Forward-mode gradients, which torch.no_grad() leaves on."""
+    import torch.autograd.forward_ad as fwd
+    from lossless_bf16_weight_nwc_b200 import paged
+    plain = torch.ones(3)
+    with fwd.dual_level():
+        dual = fwd.make_dual(plain, torch.ones(3))
+        paged._no_grad(None, plain, [1], fwd.unpack_dual(dual).primal)
+        with pytest.raises(ValueError, match="tangent"):
+            paged._no_grad(None, plain, dual)
+        with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
+            paged._no_grad(dual)
+    paged._no_grad(plain)
+
+
 def test_attention_block_arguments(lib):
     """What a step would find out after it has appended is refused when the block is made."""
     from types import SimpleNamespace as Fake
