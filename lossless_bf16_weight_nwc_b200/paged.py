@@ -462,7 +462,7 @@ class PagedKV:
         their q is zero.  q_out: q itself, or memory of no other tensor of the call
         or the cache."""
         rows, view = self._rows(batch, k, "k")
-        _no_grad(q, k, v, freq, q_weight, k_weight, q_out)
+        _no_grad(q, k, v, freq, q_weight, k_weight, q_out, self.k_pages, self.v_pages)
         device = self.device
         shape = (rows, self.kv_heads, self.dim)
         kh = _heads(k, "k", shape, device)
@@ -502,7 +502,7 @@ class PagedKV:
         exponentials.  A row that sees nothing, and a padding row, is zero (-inf).
         out: q itself, or memory of no other tensor of the call or the cache."""
         rows, view = self._rows(batch, q, "q")
-        _no_grad(q, out)
+        _no_grad(q, out, self.k_pages, self.v_pages)
         if self.dim not in (64, 128):
             raise ValueError(f"dim {self.dim}: attention takes heads of 64 or 128")
         heads = q.shape[1]

@@ -743,6 +743,25 @@ def test_gradients_are_refused_everywhere(paged):
     assert c.kv.device_error() == (0, 0)
 
 
+def test_pages_that_come_to_require_a_gradient(paged):
+    c = Case(paged, 28, [9, 30], poison=False)
+    q, k, v = (randn(c.g, 2, n, 64).bfloat16() for n in (4, 2, 2))
+    k0 = bits(c.k)
+    for pages in (c.k, c.v):
+        pages.requires_grad_()
+        for call in (lambda: c.kv.append(c.batch, k, v), lambda: c.kv.attend(c.batch, q)):
+            with pytest.raises(ValueError, match="gradient"):
+                call()
+        pages.requires_grad_(False)
+    assert torch.equal(bits(c.k), k0)
+    c.k.requires_grad_()
+    with torch.no_grad():
+        c.kv.append(c.batch, k, v)
+        got = c.kv.attend(c.batch, q)
+    c.k.requires_grad_(False)
+    c.check(q, got)
+
+
 def test_attend_unordered_groups(paged):
     """Group starts that are not ascending or point outside: some answer, nothing
     written out of bounds, and the rows outside such groups are right."""
