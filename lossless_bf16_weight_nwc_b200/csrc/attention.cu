@@ -30,6 +30,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -1532,7 +1533,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 
 template <int DIM>
 cudaError_t launch_dim(const AttentionParams& p, const PageMaps& maps, cudaStream_t stream) {
-  static bool configured[64] = {};
+  static std::atomic<bool> configured[64];   // calls may come from several threads
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -843,6 +843,76 @@ def test_other_streams_at_once(paged):
         c.check(qs[i], got[i][0])
 
 
+def test_calls_from_several_threads(paged):
+    """The first calls of a process included: each thread on a stream of its own, over
+    one cache and one batch."""
+    import threading
+    c = Case(paged, 29, [200, 31, 7], dim=128, kv_heads=4, prefix=[500], starts=[0, 2])
+    one = {n: randn(c.g, 3 * n, 8, 128).bfloat16() for n in (1, 2, 5)}
+    c.batch = paged.PagedBatch(*c.batch._keep)
+    torch.cuda.synchronize()
+    got, failed = {}, []
+
+    def work(i):
+        try:
+            torch.cuda.set_device(0)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for n in (1, 2, 5, 1):
+                    o = c.kv.attend(c.batch, one[n])
+                    r, _ = paged.qk_norm_rope(one[n], None, at[:3 * n], freq)
+                    torch.cuda.current_stream().synchronize()
+                    got[i, n] = (o, r)
+        except Exception as e:      # noqa: BLE001 (a thread's error, shown below)
+            failed.append(e)
+
+    freq, at = paged.rope_frequencies(128), torch.arange(15, device="cuda")
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for n in one:
+        want = c.kv.attend(c.batch, one[n]), paged.qk_norm_rope(one[n], None, at[:3 * n], freq)[0]
+        for i in range(6):
+            assert all(torch.equal(bits(a), bits(b)) for a, b in zip(got[i, n], want))
+        c.check(one[n], want[0])
+
+
+def test_other_streams_for_every_call(paged):
+    """The stream given and a current stream that is not the default: results are
+    allocated there, an eager run beside a captured and replayed one."""
+    g = gen(31)
+    pool = paged.PagedKV(*(randn(g, 9, 16, 2, 64).bfloat16() for _ in range(2)))
+    batch = paged.PagedBatch(torch.arange(8, device="cuda").int().view(2, 4), ints([5, 40]))
+    q, k, v = (randn(g, 2, n, 64) for n in (4, 2, 2))
+    freq, at = paged.rope_frequencies(64), ints([4, 39])
+
+    def run(stream=None):
+        a, b = paged.qk_norm_rope(q, k, at, freq, stream=stream)
+        c = pool.append(batch, k, v, q=q, freq=freq, stream=stream)
+        return a, b, c, *pool.attend(batch, c, return_lse=True, stream=stream)
+
+    want = run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = [run(side), run(side.cuda_stream)]
+    with torch.cuda.stream(side):
+        got.append(run())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got.append(run())
+    with torch.cuda.stream(side):
+        got.append(run())
+    graph.replay()
+    torch.cuda.synchronize()
+    for other in got:
+        assert all(torch.equal(x, y) for x, y in zip(other, want))
+    assert pool.device_error(side) == (0, 0)
+
+
 def test_graph_replays_follow_lengths(paged):
     """A captured append + attend replayed as the sequences grow; two graphs of
     one cache keep their own workspace."""
