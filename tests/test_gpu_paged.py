@@ -80,6 +80,48 @@ def test_qk_norm_rope(paged, tokens, h, hk, dim, rotary, inter, wkind, tin, tout
     assert torch.equal(y, before)
 
 
+LARGE = [  # as QK: enough tokens to fill the device, odd numbers of them
+    (1301, 32, 8, 128, 128, False, "bf16", "bf16", "bf16"),
+    (1301, 32, 8, 128, 128, True, "f32", "f32", "bf16"),
+    (1203, 28, 4, 128, 128, False, None, "f32", "f32"),
+    (1302, 12, 4, 64, 64, False, "bf16", "f32", "bf16"),
+    (1303, 8, 8, 64, 64, True, "bf16", "bf16", "bf16"),
+    (1299, 4, 4, 64, 64, True, None, "bf16", "f32"),
+    (1201, 3, 1, 256, 256, True, "f32", "bf16", "bf16"),
+    (1301, 7, 3, 128, 128, False, "bf16", "bf16", "bf16"),
+    (1305, 6, 2, 96, 96, False, "bf16", "bf16", "bf16"),
+    (1205, 32, 8, 128, 64, False, "bf16", "f32", "bf16"),
+    (1205, 32, 8, 128, 0, False, "bf16", "bf16", "bf16"),
+]
+
+
+@pytest.mark.parametrize("tokens,h,hk,dim,rotary,inter,wkind,tin,tout", LARGE)
+@pytest.mark.parametrize("form", ["both", "q", "k", "unaligned", "in place"])
+def test_qk_norm_rope_of_prompts(paged, tokens, h, hk, dim, rotary, inter, wkind, tin, tout, form):
+    """The forms that take several tokens a block: of whole heads and general, aligned
+    and not, with q or k alone and in place."""
+    g = gen(tokens + dim + rotary)
+    off = 1 if form == "unaligned" else 0
+    y = (2 * randn(g, tokens, (h + 2 * hk) * dim + off)).to(DT[tin])[:, off:]
+    q, k, _ = (t.unflatten(1, (-1, dim)) for t in y.split([h * dim, hk * dim, hk * dim], 1))
+    pos = torch.randint(0, 200000, (tokens,), generator=g, device="cuda")
+    freq = paged.rope_frequencies(rotary, 1e4) if rotary else None
+    qw, kw = weights(g, wkind, dim), weights(g, wkind, dim)
+    want = [ref.norm_rotate(x, w, pos, freq, inter, 1e-6) for x, w in ((q, qw), (k, kw))]
+    if form == "in place":
+        out, tout = (q, k), tin
+        v0 = y[:, -hk * dim:].clone()
+    else:
+        out = [torch.full(t.shape, math.nan, dtype=DT[tout], device="cuda") for t in (q, k)]
+        y0 = y.clone()
+    give = {"q": (q, None), "k": (None, k)}.get(form, (q, k))
+    paged.qk_norm_rope(*give, pos, freq, qw, kw, interleaved=inter,
+                       out=tuple(o if x is not None else None for o, x in zip(out, give)))
+    for x, got, (w, bound) in zip(give, out, want):
+        assert x is None and torch.isnan(got).all() or ref.close(got, w, bound, DT[tout])
+    assert torch.equal(y[:, -hk * dim:], v0) if form == "in place" else torch.equal(y, y0)
+
+
 def test_qk_far_and_negative_positions(paged):
     g = gen(1)
     pos = torch.tensor([0, -1, -5000, 2 ** 31 - 1, 2 ** 40 + 3, 10 ** 6], device="cuda")
@@ -285,6 +327,41 @@ def test_append_large_batches_and_heads(paged):
         want, bound = ref.norm_rotate(k, None, pos, freq, False, 0)
         assert ref.close(c.k[at], want, bound, torch.bfloat16)
         assert torch.equal(c.v[at], v)
+
+
+@pytest.mark.parametrize("hk,h,dim,rotary", [(8, 32, 128, 128), (4, 8, 64, 64), (1, 5, 256, 256),
+                                              (8, 32, 128, 64), (3, 6, 80, 80)])
+@pytest.mark.parametrize("tin,inter,norm", [("bf16", False, True), ("f32", True, True),
+                                            ("bf16", True, False)])
+def test_append_of_prompts(paged, hk, h, dim, rotary, tin, inter, norm):
+    """Chunks of odd length, padded at their ends: a block's tokens change from padding
+    to tokens, from one sequence to the next, in every place."""
+    lens, chunk, q_lens = [499, 40, 700, 0, 503], 501, [499, 2, 501, 0, 3]
+    c = Case(paged, 30 + dim, lens, q_lens=q_lens, kv_heads=hk, dim=dim, poison=False,
+             prefix=[77], starts=[1, 4])
+    rows = len(lens) * chunk
+    y = randn(c.g, rows, (h + 2 * hk) * dim).to(DT[tin])
+    q, k, v = (t.unflatten(1, (-1, dim)) for t in y.split([h * dim, hk * dim, hk * dim], 1))
+    freq = paged.rope_frequencies(rotary, 1e4)
+    w = weights(c.g, "bf16", dim) if norm else None
+    k0, v0 = c.k.clone(), c.v.clone()
+    out = torch.full(q.shape, math.nan, dtype=torch.bfloat16, device="cuda")
+    c.kv.append(c.batch, k, v, q=q, freq=freq, q_weight=w, k_weight=w, interleaved=inter,
+                q_out=out)
+    i = torch.arange(chunk, device="cuda")
+    real = (i < ints(q_lens)[:, None]).flatten()
+    j = ((ints(lens) - ints(q_lens))[:, None] + i).flatten()
+    seq = torch.arange(len(lens), device="cuda").repeat_interleave(chunk)
+    pos = j + 77 * ((seq >= 1) & (seq < 4))
+    want, bound = ref.norm_rotate(q, w, pos, freq, inter, 1e-6)
+    assert ref.close(out[real], want[real], bound[real], torch.bfloat16) and not out[~real].any()
+    at = (c.table[seq[real], j[real] // 16].long(), j[real] % 16)
+    want, bound = ref.norm_rotate(k, w, pos, freq, inter, 1e-6)
+    assert ref.close(c.k[at], want[real], bound[real], torch.bfloat16)
+    assert torch.equal(c.v[at], v[real].bfloat16())
+    c.k[at], c.v[at] = k0[at], v0[at]
+    assert torch.equal(bits(c.k), bits(k0)) and torch.equal(bits(c.v), bits(v0))
+    assert c.kv.device_error() == (0, 0)
 
 
 def test_append_in_place(paged):
