@@ -415,7 +415,9 @@ typedef struct {
  *     d_group_start[g] .. d_group_start[g + 1] - 1 share the prefix of
  *     d_prefix_lens[g] tokens in pages d_prefix_table[g prefix_stride + n],
  *     n < prefix_width, which comes before their own tokens.  Sequences in no
- *     group have no prefix.  groups = 0: none has.
+ *     group have no prefix.  groups = 0: none has.  (Of groups that overlap, which
+ *     are a mistake, a sequence has the first; attention sets error bit 4 and leaves
+ *     prefixes out where their rows are more than its workspace is for.)
  * Lengths below zero count as zero.  A real row whose index is then negative (more
  * new tokens than the sequence has) has no place: it is not appended, its q is normed
  * and rotated at its position, and in attention it sees its prefix and no own token.

@@ -854,6 +854,88 @@ def test_attend_unordered_groups(paged):
     c.check(q, got, lse)
 
 
+def attend_c(paged, c, batch, q, chunk=1):
+    """(out, lse) through the C call's own structures, with a workspace of the stated size
+    between bytes that have to stay."""
+    from lossless_bf16_weight_nwc_b200 import _lib
+    rows, heads, dim = q.shape
+    view = _lib.nwc_kv_batch.from_address(batch._view(rows))
+    need = _lib.nwc_kv_attention_workspace(c.kv._view, view, heads)
+    ws = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((rows, heads), 7.0, device="cuda")
+    qv, ov = (_lib.nwc_heads.from_buffer_copy(paged._heads(t, "t", t.shape, t.device))
+              for t in (q, out))
+    _lib.nwc_kv_attention(c.kv._view, view, qv, heads, dim ** -0.5, ov, lse, ws[4096:], need)
+    assert bool((ws[:4096] == 0xA5).all()) and bool((ws[4096 + need:] == 0xA5).all())
+    return out, lse
+
+
+@pytest.mark.parametrize("starts", [[4, 2, 9, 1], [-3, 0, 100, 100], [8, 8, 8, 8], [0, 8, 0, 8],
+                                    [2, 5, 5, 5], [0, 0, 0, 8], [9, -1, 3, 2]])
+@pytest.mark.parametrize("chunk,heads", [(1, 4), (5, 8), (40, 8)])
+def test_attend_unordered_groups_values(paged, starts, chunk, heads):
+    """Group starts out of order or outside: sequences that no group holds have no
+    prefix, those that one group holds have its, and nothing is written elsewhere."""
+    c = Case(paged, 32, [40] * 8, prefix=[500, 300, 100], starts=[0, 2, 4, 8])
+    q = randn(c.g, 8 * chunk, heads, 64).bfloat16()
+    batch = paged.PagedBatch(c.table, ints(c.lens), None, c.far, ints(c.prefix), ints(starts))
+    out, lse = attend_c(paged, c, batch, q)
+    held = [[g for g in range(3) if starts[g] <= b < starts[g + 1]] for b in range(8)]
+    for b, groups in enumerate(held):
+        rows = slice(b * chunk, (b + 1) * chunk)
+        if len(groups) < 2:
+            far = (c.far[groups], [c.prefix[groups[0]]], [0, 1]) if groups else (None, None, None)
+            want, bound, want_lse, lse_bound = ref.attention(
+                q[rows], c.k, c.v, c.table[b:b + 1], [40], None, *far, 1 / 8)
+            assert ref.close(out[rows], want, bound, torch.bfloat16)
+            assert bool(((lse[rows].double() - want_lse).abs() <= lse_bound).all())
+    # Two groups over 1280 rows of a key head are 5 blocks x 2 heads each: 20 items, where
+    # the workspace of 1280 rows and 3 groups has (5 + 3) x 2.
+    overlap = any(len(groups) > 1 for groups in held)
+    assert c.kv.device_error() == ((1, 4) if overlap and chunk == 40 else (0, 0))
+
+
+def test_attend_groups_that_overlap(paged):
+    """More rows in groups than there are rows: reported, nothing written elsewhere,
+    and the next call is right."""
+    n = 128
+    c = Case(paged, 33, [9] * n, prefix=[200] * 8, starts=[16 * i for i in range(9)])
+    q = randn(c.g, n, 16, 64).bfloat16()
+    batch = paged.PagedBatch(c.table, ints(c.lens), None, c.far, ints(c.prefix),
+                             ints([0, n] * 4 + [0]))
+    attend_c(paged, c, batch, q)
+    assert c.kv.device_error() == (1, 4)
+    c.check(q, *attend_c(paged, c, c.batch, q))
+
+
+def test_typed_calls(paged):
+    """The C calls with _lib's structures give what the Python calls do."""
+    from lossless_bf16_weight_nwc_b200 import _lib
+    c = Case(paged, 34, [9, 30], poison=False)
+    q, k, v = (randn(c.g, 2, n, 64) for n in (4, 2, 2))
+    freq, at, w = paged.rope_frequencies(64), ints([8, 29]), weights(c.g, "f32", 64)
+
+    def view(t):
+        return _lib.nwc_heads.from_buffer_copy(paged._heads(t, "t", t.shape, t.device))
+
+    rope = _lib.nwc_rope.from_buffer_copy(paged._rope(64, q.device, freq, w, w, 1e-6, True))
+    batch = _lib.nwc_kv_batch.from_address(c.batch._view(2))
+    want = paged.qk_norm_rope(q, k, at, freq, w, w, interleaved=True)
+    got = [torch.empty_like(t) for t in want]
+    _lib.nwc_qk_norm_rope(view(q), view(k), view(got[0]), view(got[1]), 2, 4, 2, 64, at, False,
+                          rope)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    rotated = torch.empty_like(got[0])
+    _lib.nwc_kv_append(c.kv._view, batch, view(q), view(rotated), 4, view(k), view(v), rope)
+    assert torch.equal(rotated, got[0])
+    place = c.table[[0, 1], [0, 1]].long(), torch.tensor([8, 13], device="cuda")
+    assert torch.equal(c.k[place], got[1]) and torch.equal(c.v[place], v.bfloat16())
+    out, lse = attend_c(paged, c, c.batch, rotated)
+    assert torch.equal(out, c.kv.attend(c.batch, rotated))
+    c.check(rotated, out, lse)
+    assert _lib.nwc_kv_get_error(c.kv._view) == (0, 0)
+
+
 def test_attend_shared_pages_and_repeats(paged):
     """Sequences that point at the same pages, and a prefix whose pages repeat."""
     c = Case(paged, 14, [64, 64, 64], prefix=[64], starts=[0, 3], poison=False)
