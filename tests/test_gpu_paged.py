@@ -1160,3 +1160,42 @@ def test_attention_block(paged, batch_rows):
         assert rel <= 2.0 ** -8 * (3 + 4 * top)
         at += chunk
     assert kv.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("rows", [1, 20, 61])
+def test_attention_block_captured(paged, rows):
+    """A captured step replayed token after token gives the eager steps' bits; lengths
+    and inputs change in place."""
+    from lossless_bf16_weight_nwc_b200 import _lib, synth
+    hidden, h, hk, dim = 512, 8, 2, 64
+    w = [synth.matrix(synth.MatrixSpec("w", r, c, "normal", 0.06, 0), i)
+         for i, (r, c) in enumerate([(h * dim, hidden), (hk * dim, hidden), (hk * dim, hidden),
+                                     (hidden, h * dim)])]
+    wqkv, wo = _lib.CompressedMatrix.compress_fused(w[:3]), _lib.CompressedMatrix.compress(w[3])
+    freq, sides = paged.rope_frequencies(dim), []
+    table = torch.randperm(3 * rows, generator=gen(41), device="cuda").int().view(rows, 3)
+    for _ in range(2):
+        kv = paged.PagedKV(*(torch.zeros(3 * rows, 16, hk, dim, dtype=torch.bfloat16,
+                                         device="cuda") for _ in range(2)))
+        lens = ints([1 + i % 7 for i in range(rows)])
+        sides.append((paged.AttentionBlock(wqkv, wo, kv, freq), paged.PagedBatch(table, lens),
+                      lens, kv))
+    g = gen(42)
+    x = randn(g, rows, hidden).bfloat16()
+    block, batch, lens, kv = sides[1]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block.step(x, batch)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = block.step(x, batch)
+    for _ in range(30):
+        want = sides[0][0].step(x, sides[0][1])
+        graph.replay()
+        assert torch.equal(y, want) and torch.equal(bits(kv.k_pages), bits(sides[0][3].k_pages))
+        x.copy_(randn(g, rows, hidden))
+        for s in sides:
+            s[2].add_(1)
+    assert kv.device_error() == (0, 0) and wqkv.device_error() == (0, 0)
