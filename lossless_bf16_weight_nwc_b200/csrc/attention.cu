@@ -651,13 +651,11 @@ __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* ba
 
   // A wait that gives up may do so for some lanes only: the warp goes by all of them,
   // as it meets again in votes and barriers of all lanes.
-  auto arrived = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(kAll, wait(bar, parity, ctl));
-  };
   auto issue_s = [&](const Unit& u, uint32_t w) -> bool {
-    if (u.first && !arrived(&bars->qfull[w], q_turn[w]++ & 1u)) return false;
     const uint32_t seq = 2 * u.tile, slot = seq % L::kRing;
-    if (!arrived(&bars->full[slot], (seq / L::kRing) & 1u)) return false;
+    const bool ready = (!u.first || wait(&bars->qfull[w], q_turn[w]++ & 1u, ctl)) &&
+                       wait(&bars->full[slot], (seq / L::kRing) & 1u, ctl);
+    if (!__all_sync(kAll, ready)) return false;
     tc_fence_after();
     const uint64_t a = umma_desc_sw128(q + w * L::kTile);
     const uint64_t b = umma_desc_sw128(ring + slot * L::kTile);
@@ -670,9 +668,10 @@ __device__ void issue_products(const AttentionParams& p, uint8_t* smem, Bars* ba
     return true;
   };
   auto issue_o = [&](const Unit& u, uint32_t w) -> bool {
-    if (!arrived(&bars->pfull[w], p_turn[w]++ & 1u)) return false;
     const uint32_t seq = 2 * u.tile + 1, slot = seq % L::kRing;
-    if (!arrived(&bars->full[slot], (seq / L::kRing) & 1u)) return false;
+    const bool ready = wait(&bars->pfull[w], p_turn[w]++ & 1u, ctl) &&
+                       wait(&bars->full[slot], (seq / L::kRing) & 1u, ctl);
+    if (!__all_sync(kAll, ready)) return false;
     tc_fence_after();
     const uint64_t b = umma_desc_mn_sw128(ring + slot * L::kTile, kKvTile * 128u);
 #pragma unroll
