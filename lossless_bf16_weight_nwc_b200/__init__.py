@@ -10,7 +10,8 @@ rotation, a paged key/value cache, attention over shared prefixes).
 """
 import importlib
 
-__all__ = ["CompressedMatrix", "PagedBatch", "PagedKV", "lib"]
+_PAGED = ("AttentionBlock", "PagedBatch", "PagedKV", "qk_norm_rope", "rope_frequencies")
+__all__ = ["CompressedMatrix", "lib", *_PAGED]
 
 
 def __getattr__(name):
@@ -18,6 +19,6 @@ def __getattr__(name):
         return importlib.import_module(__name__ + "._lib")
     if name == "CompressedMatrix":
         return importlib.import_module(__name__ + "._lib").CompressedMatrix
-    if name in ("PagedBatch", "PagedKV"):
+    if name in _PAGED:
         return getattr(importlib.import_module(__name__ + ".paged"), name)
     raise AttributeError(name)

@@ -228,6 +228,16 @@ def test_outputs_with_gaps(lib):
             paged._heads(bad, "o", bad.shape, cpu, output=True)
 
 
+def test_package_names(lib):
+    import lossless_bf16_weight_nwc_b200 as package
+    from lossless_bf16_weight_nwc_b200 import paged
+    for name in ("AttentionBlock", "PagedBatch", "PagedKV", "qk_norm_rope", "rope_frequencies"):
+        assert name in package.__all__ and getattr(package, name) is getattr(paged, name)
+    assert all(hasattr(package, name) for name in package.__all__)
+    with pytest.raises(AttributeError):
+        package.no_such_name
+
+
 def test_tangents_are_refused(lib):
     """Forward-mode gradients, which torch.no_grad() leaves on."""
     import torch.autograd.forward_ad as fwd
