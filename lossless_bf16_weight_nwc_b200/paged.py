@@ -69,13 +69,13 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, device="cuda",
 def _no_grad(*tensors) -> None:
     if _grad_enabled():
         for t in tensors:
-            if isinstance(t, torch.Tensor) and t.requires_grad:
+            if t is not None and isinstance(t, _Tensor) and t.requires_grad:
                 raise ValueError("a tensor requires a gradient, which these kernels do not "
                                  "give; call under torch.no_grad()")
     # (The level saves asking every tensor where no dual level is open.)
     if getattr(forward_ad, "_current_level", 0) >= 0:
         for t in tensors:
-            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            if isinstance(t, _Tensor) and forward_ad.unpack_dual(t).tangent is not None:
                 raise ValueError("a tensor has a tangent, a forward-mode gradient that these "
                                  "kernels do not carry on; unpack it first")
 
