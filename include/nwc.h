@@ -421,9 +421,9 @@ typedef struct {
  * Lengths below zero count as zero.  A real row whose index is then negative (more
  * new tokens than the sequence has) has no place: it is not appended, its q is normed
  * and rotated at its position, and in attention it sees its prefix and no own token.
- * A token beyond its table (or the 2^30th), or
- * on a page outside [0, pages), sets error bit 4: it is not appended, and
- * attention sees no token past the table and zeros for the page.
+ * A token beyond its table (or the 2^30th), or on a page outside [0, pages), sets
+ * error bit 4: it is not appended, and attention sees no token past the table and
+ * zeros for the page.
  * sequences x new_tokens <= 2^24; groups <= sequences.  A table of width 0 holds no
  * page (and may be NULL). */
 typedef struct {
@@ -476,8 +476,10 @@ nwc_status nwc_kv_attention_workspace(const nwc_kv_cache* cache, const nwc_kv_ba
  *     overlaps must not share it.
  * A row that sees no token, and a padding row, is zero with d_lse -infinity.
  * Scores, sums and the running maximum are FP32; a probability is rounded to
- * BF16 before it multiplies V.  Memory behind a sequence's or a prefix's last
- * token, and tokens that a row does not see, play no part in it, whatever they hold.
+ * BF16 (to nearest) before it multiplies V.  The weights of a sum are up to 2^8, so
+ * sums of |V| over a row's tokens should stay below 2^120.  Memory behind a
+ * sequence's or a prefix's last token, and tokens that a row does not see, play no
+ * part in it, whatever they hold.
  * The result is the same bit pattern on every run.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA (launch). */
 nwc_status nwc_kv_attention(const nwc_kv_cache* cache, const nwc_kv_batch* batch,

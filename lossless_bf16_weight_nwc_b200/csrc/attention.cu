@@ -23,10 +23,13 @@
 // A second kernel joins the parts' results in a fixed order.
 //
 // B200, 32 query heads over 8 key heads of 128: 64 sequences of 100 to 1900 own tokens
-// behind 32768 shared ones take 89 us (406 MB, 4.6 TB/s, 0.70 of a copy's rate); 64
-// without a prefix 55 us (0.71); 64 rows of one sequence over 16400 tokens 41 us (420
-// TFLOP/s): 13 us of a start, Q and results around 7 tiles a CTA; one row over 1003
-// tokens 12 us, of which 4 in the second kernel.
+// behind 32768 shared ones take 91 us in a burst (406 MB, 4.5 TB/s, 0.68 of a copy's
+// rate), 97 to 100 in loops that last, where the power cap lowers the clock; the 64
+// without a prefix 52 us (0.67), of 2000 to 6000 tokens each 174 us (0.96); 64 rows of
+// one sequence over 16400 tokens 41 us (420 TFLOP/s): 13 us of a start, Q and results
+// around 7 tiles a CTA; one row over 1003 tokens 12 us, of which 4 in the second kernel.
+// A prompt taken in one call also multiplies the tiles that its rows do not see (4096
+// rows: 557 us, 247 TFLOP/s of what they see).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -16,7 +16,9 @@
 // by the chain of loads, so those get a block for every four warps' heads.
 //
 // B200, 32 + 8 heads of 128: q and k of 8192 tokens from BF16 42 us (168 MB, 4.0 TB/s);
-// appending 4 x 1024 rows of which 2519 are real 21 us; 64 tokens 3.8 us, one 3.2 us.
+// appending 4 x 1024 rows of which 2519 are real 20.5 us; 64 tokens 3.8 us, one 3.2 us.
+// From FP32 70 us (252 MB, 3.6 TB/s); in the general form half of each head 54 us, heads
+// of 96 53 us (126 MB).
 // Five blocks an SM measured best (four 45 us, six 46), as did four tokens a block (eight
 // 48 us; twelve 41, but 40 for the ragged append), and eight elements a lane (sixteen,
 // with fewer instructions and fewer warps: 43).

@@ -334,7 +334,8 @@ class PagedBatch:
     prefix_table int32 [groups, width], prefix_lens int32 [groups], group_start
                  int32 [groups + 1]: sequences group_start[g] up to
                  group_start[g + 1] share prefix g, which comes before their own
-                 tokens; all three or none.
+                 tokens; all three or none, no more groups than sequences (groups
+                 may be empty).
 
     All on one CUDA device; their contents are read when a kernel runs, so they
     may be changed in place between calls.  Entries behind a sequence's last page
@@ -460,7 +461,7 @@ class PagedKV:
         FP32 or BF16, one type, with any strides but a contiguous last dimension.
         seq_lens counts the new tokens already.  Padding rows are not appended,
         their q is zero.  q_out: q itself, or memory of no other tensor of the call
-        or the cache."""
+        or the cache; k and v may lie in pages, but not where the call appends."""
         rows, view = self._rows(batch, k, "k")
         _no_grad(q, k, v, freq, q_weight, k_weight, q_out, self.k_pages, self.v_pages)
         device = self.device
