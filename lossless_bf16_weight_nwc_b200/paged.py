@@ -154,15 +154,16 @@ def _bytes(t):
 
 def _apart(out, what: str, source, *others) -> None:
     """Refuses an output in memory of another tensor of its call, whose kernels read
-    while they write; `source` (an input of its shape) may be the output itself."""
+    while they write; `source` (an input of its shape) may be the output itself, but
+    not in a second part of the call."""
     at, end = _bytes(out)
-    for t in (source, *others):
+    for i, t in enumerate((source, *others)):
         if t is None:
             continue
         first, behind = _bytes(t)
         if behind <= at or end <= first or first == behind or at == end:
             continue
-        if (t is source and first == at and t.dtype == out.dtype and
+        if (i == 0 and first == at and t.dtype == out.dtype and
                 all(n < 2 or s == o for n, s, o in zip(t.shape, t.stride(), out.stride()))):
             continue
         if t.dim() != 3 or _meet(out, t):

@@ -313,7 +313,7 @@ def test_outputs_apart(lib):
             (k, k, (q, y)), (q[1:], q[:-1], ()), (full[:5].bfloat16(), None, ()),
             (torch.as_strided(full.view(torch.bfloat16), (5, 4, 8), (64, 16, 1)), full[:5], ()),
             (torch.as_strided(full, (5, 4, 8), (32, 8, 1)), full[:5].transpose(0, 1), ()),
-            (full[:5], None, (full[4, 3],)), (q, q, (y[:, 31:40],))):
+            (full[:5], None, (full[4, 3],)), (q, q, (y[:, 31:40],)), (q, q, (q,))):
         if others or source is not None:
             with pytest.raises(ValueError, match="overlaps"):
                 paged._apart(out, "o", source, *others)
