@@ -957,6 +957,76 @@ def test_attend_strides(paged):
     assert not store[:, 0].any() and not store[..., :8].any()
 
 
+@pytest.mark.parametrize("layout", ["K beside V", "gaps", "heads outside", "V is K", "large pages"])
+def test_page_layouts(paged, layout):
+    """Pages that are views: of one tensor for K and V, with gaps between heads and
+    tokens, with heads outside pages, the same tensor twice, pages longer than a tile."""
+    g, page, hk, dim = gen(50), 16, 3, 64
+    if layout == "K beside V":
+        k, v = randn(g, 30, 2, page, hk, dim).bfloat16().unbind(1)
+    elif layout == "gaps":
+        k, v = (randn(g, 30, page + 1, hk + 2, dim + 8).bfloat16()[:, :page, 1:hk + 1, 8:]
+                for _ in range(2))
+    elif layout == "heads outside":
+        k, v = (randn(g, hk, 30, page, dim).bfloat16().permute(1, 2, 0, 3) for _ in range(2))
+    elif layout == "V is K":
+        k = v = randn(g, 30, page, hk, dim).bfloat16()
+    else:
+        page = 4096
+        k, v = (randn(g, 4, page, hk, dim).bfloat16() for _ in range(2))
+    pool = paged.PagedKV(k, v)
+    own = (torch.randperm(k.shape[0], generator=g, device="cuda").int()
+           if page > 16 else torch.randperm(30, generator=g, device="cuda").int()[:28])
+    table, far = (own[:2].view(2, 1), own[2:].view(1, 2)) if page > 16 else (
+        own[:20].view(2, 10), own[20:].view(1, 8))
+    lens, prefix = ([3000, 129], [4099]) if page > 16 else ([155, 17], [120])
+    batch = paged.PagedBatch(table, ints(lens), None, far, ints(prefix), ints([0, 2]))
+    new = [randn(g, 4, hk, dim) for _ in range(2)]
+    k0, v0 = k.clone(), v.clone()
+    if layout != "V is K":
+        pool.append(batch, *new)
+        for b, n in enumerate(lens):
+            for i in range(2):
+                at = int(table[b, (n - 2 + i) // page]), (n - 2 + i) % page
+                k0[at], v0[at] = new[0][2 * b + i].bfloat16(), new[1][2 * b + i].bfloat16()
+        assert torch.equal(k, k0) and torch.equal(v, v0)
+    for heads, chunk in ((3, 1), (12, 2), (24, 40 if page > 16 else 17)):
+        q = randn(g, 2 * chunk, heads, dim).bfloat16()
+        got, lse = pool.attend(batch, q, return_lse=True)
+        want, bound, want_lse, lse_bound = ref.attention(q, k, v, table, lens, None, far, prefix,
+                                                         [0, 2], 1 / 8)
+        assert ref.close(got, want, bound, torch.bfloat16)
+        assert bool(((lse.double() - want_lse).abs() <= lse_bound).all())
+    assert pool.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("heads,kw", [(1, dict(kv_heads=1)), (8, dict(kv_heads=2, dim=128))])
+def test_attend_many_sequences_and_groups(paged, heads, kw):
+    """More segments than a CTA's first look at them holds, empty groups among them."""
+    n, groups = 2600, 900
+    starts = [0] + sorted((i * 7919) % n for i in range(groups - 1)) + [n]
+    c = Case(paged, 51, [(i * 37) % 50 for i in range(n)], page=8,
+             prefix=[(i * 53) % 70 for i in range(groups)], starts=starts, **kw)
+    q = randn(c.g, n, heads, c.kv.dim).bfloat16()
+    got, lse = c.kv.attend(c.batch, q, return_lse=True)
+    c.check(q, got, lse)
+
+
+@pytest.mark.parametrize("own,far,chunk", [(2 ** 20 + 3, 0, 1), (5, 2 ** 20 + 77, 1),
+                                           (2 ** 19 + 1, 2 ** 19, 33)])
+def test_attend_long(paged, own, far, chunk):
+    """A million tokens: sums of 2^20 terms over all CTAs."""
+    kw = dict(prefix=[far], starts=[0, 1]) if far else {}
+    c = Case(paged, 52, [own], kv_heads=1, page=64, **kw)
+    q = (2 * randn(c.g, chunk, 2, 64)).bfloat16()
+    got, lse = c.kv.attend(c.batch, q, return_lse=True)
+    want, bound, want_lse, lse_bound = c.want(q, 1 / 8)
+    assert ref.close(got, want, bound, torch.bfloat16)
+    # 64 sums in a tile, 56 tiles a CTA, up to 300 parts: 420 roundings of 2^-24.
+    assert bool(((lse.double() - want_lse).abs() <= lse_bound + 2.0 ** -15).all())
+    assert c.kv.device_error() == (0, 0)
+
+
 def test_attend_far_offsets(paged):
     """Pages whose offsets pass 2^32 elements."""
     pages, page, hk, dim = 70000, 128, 8, 64
